@@ -13,7 +13,8 @@ quest_update_meta, quest_score_pages, quest_topk_pages, quest_sparse_attn,
 quest_decode_attn, the 8-bit cache calls gqa_decode_attn_e4m3 /
 kv_append_e4m3 and their Quest counterparts (quest_append_kv_e4m3,
 quest_update_meta_e4m3, quest_score_pages_e4m3, quest_sparse_attn_e4m3), the
-4-bit pair and prefill.
+4-bit pair, prefill, and the paged serving calls (paged_build_tables,
+paged_release_pages, paged_norm_rope_append, gqa_paged_attn).
 """
 from __future__ import annotations
 
@@ -37,6 +38,10 @@ GQAQ_DEV_TIMEOUT = 1
 GQAQ_DEV_BAD_LEN = 2
 GQAQ_DEV_BAD_PAGE = 4
 GQAQ_DEV_BAD_POS = 8
+GQAQ_DEV_NO_PAGES = 16
+
+GQAQ_F16 = 0
+GQAQ_BF16 = 1
 
 GQAQ_OPT_MAX_CTAS = 1
 GQAQ_OPT_WAIT_TIMEOUT_NS = 2
@@ -64,6 +69,11 @@ class Dims(ctypes.Structure):
                 ("max_len", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
+class PagedDims(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("batch", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
+                                                  "num_pages", "max_pages", "max_tokens", "dtype")]
+
+
 # Exported symbols, in the order include/gqaq.h declares them.
 EXPORTS = ("gqaq_workspace_bytes", "gqa_decode_attn", "quest_append_kv", "quest_update_meta",
            "quest_score_pages", "quest_topk_pages", "quest_sparse_attn", "quest_decode_attn",
@@ -72,6 +82,8 @@ EXPORTS = ("gqaq_workspace_bytes", "gqa_decode_attn", "quest_append_kv", "quest_
            "quest_decode_attn_e4m3",
            "gqa_decode_attn_int4", "kv_append_int4",
            "gqaq_prefill_workspace_bytes", "gqa_prefill_attn",
+           "paged_build_tables", "paged_release_pages", "paged_norm_rope_append", "gqaq_paged_workspace_bytes",
+           "gqa_paged_attn",
            "gqaq_status_string", "gqaq_set_option", "gqaq_device_status", "gqaq_version")
 
 _lib = None
@@ -112,13 +124,22 @@ def lib():
         L.gqaq_prefill_workspace_bytes.argtypes = [dp, i32]
         L.gqaq_prefill_workspace_bytes.restype = ctypes.c_size_t
         L.gqa_prefill_attn.argtypes = [dp, i32, vp, vp, vp, vp, f32, vp, vp, ctypes.c_size_t, vp]
+        pd, i64 = ctypes.POINTER(PagedDims), ctypes.c_int64
+        L.paged_build_tables.argtypes = [pd] + [vp] * 11
+        L.paged_release_pages.argtypes = [pd] + [vp] * 7
+        L.paged_norm_rope_append.argtypes = [pd, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, f32, vp, i32, i32, i32, vp, vp,
+                                             vp, vp]
+        L.gqaq_paged_workspace_bytes.argtypes = [pd]
+        L.gqaq_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.gqa_paged_attn.argtypes = [pd, i32, vp, vp, vp, vp, vp, vp, f32, vp, vp, ctypes.c_size_t, vp]
         L.gqaq_status_string.argtypes = [i32]
         L.gqaq_status_string.restype = ctypes.c_char_p
         L.gqaq_set_option.argtypes = [i32, ctypes.c_int64]
         L.gqaq_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), i32]
         L.gqaq_version.argtypes = []
         for name in EXPORTS:
-            if name not in ("gqaq_workspace_bytes", "gqaq_status_string", "gqaq_prefill_workspace_bytes"):
+            if name not in ("gqaq_workspace_bytes", "gqaq_status_string", "gqaq_prefill_workspace_bytes",
+                            "gqaq_paged_workspace_bytes"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -634,3 +655,201 @@ def new_meta(batch: int, num_kv_heads: int, max_len: int, head_dim: int, device,
     """Allocate a metadata buffer [B,Hkv,Pmax,2,D] fp16 (contents undefined)."""
     return torch.empty(batch, num_kv_heads, num_pages(max_len, page_size), 2, head_dim,
                        dtype=torch.float16, device=device)
+
+
+# ---------------------------------------------------------------------------
+# Paged caches
+# ---------------------------------------------------------------------------
+_PAGED_DTYPES = {torch.float16: GQAQ_F16, torch.bfloat16: GQAQ_BF16}
+
+
+def make_paged_dims(batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages, max_tokens,
+                    dtype=torch.float16) -> PagedDims:
+    """Shape of a paged step; dtype is torch.float16 or torch.bfloat16."""
+    if dtype not in _PAGED_DTYPES:
+        raise ValueError(f"paged caches hold torch.float16 or torch.bfloat16, not {dtype}")
+    return PagedDims(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size), int(num_pages),
+                     int(max_pages), int(max_tokens), _PAGED_DTYPES[dtype])
+
+
+def paged_dims_of(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor) -> PagedDims:
+    T, Hq, D = q.shape
+    num_pages, Hkv, S, _ = k_pages.shape
+    B, max_pages = block_table.shape
+    return make_paged_dims(B, Hq, Hkv, D, S, num_pages, max_pages, T, q.dtype)
+
+
+def paged_workspace_bytes(dims: PagedDims) -> int:
+    n = lib().gqaq_paged_workspace_bytes(ctypes.byref(dims))
+    if n == 0:
+        raise GqaqError("gqaq_paged_workspace_bytes", GQAQ_ERR_UNSUPPORTED, "dims rejected")
+    return int(n)
+
+
+def alloc_paged_workspace(dims: PagedDims, device) -> torch.Tensor:
+    """Zero-filled workspace for gqa_paged_attn (its counters stay zero between calls).
+    Its size depends on head_dim and the device only, so one serves every batch and every layer in a stream."""
+    return torch.zeros(paged_workspace_bytes(dims), dtype=torch.uint8, device=device)
+
+
+def new_pages(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device,
+              dtype=torch.float16) -> torch.Tensor:
+    """Allocate one pool of pages [num_pages,Hkv,S,D] (contents undefined)."""
+    return torch.empty(num_pages, num_kv_heads, page_size, head_dim, dtype=dtype, device=device)
+
+
+def _paged(name: str, t, dtype, shape):
+    """A contiguous CUDA tensor of this dtype and shape on the current device (None in shape: any extent)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    got = t.shape
+    if len(got) != len(shape):
+        raise ValueError(f"{name} must have {len(shape)} dims, got {tuple(got)}")
+    for have, want in zip(got, shape):
+        if want is not None and have != want:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _paged_stream(*tensors) -> int:
+    """The current stream of the current device, which must hold every tensor."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def paged_build_tables(cache_len, new_len, free_pages, free_count, block_table, max_tokens: int,
+                       page_size: int = PAGE_SIZE, kv_len=None, cu_q=None, positions=None, slots=None,
+                       free_count_out=None):
+    """Plan a paged step on the GPU from cache_len / new_len [B]: take pages off the end of
+    free_pages[:free_count], write them to block_table [B,max_pages], and return
+    (kv_len [B], cu_q [B+1], positions [max_tokens], slots [max_tokens], free_count_out [1]), all int32.
+    Requests are served in order, each wholly or not at all; a refused one has kv_len 0 and slots -1.
+    free_count_out may be free_count itself; without it a new tensor holds the count."""
+    i32 = torch.int32
+    B = cache_len.shape[0] if cache_len.dim() == 1 else -1
+    T = int(max_tokens)
+    dev = cache_len.device
+    kv_len = torch.empty(B, dtype=i32, device=dev) if kv_len is None else kv_len
+    cu_q = torch.empty(B + 1, dtype=i32, device=dev) if cu_q is None else cu_q
+    positions = torch.empty(T, dtype=i32, device=dev) if positions is None else positions
+    slots = torch.empty(T, dtype=i32, device=dev) if slots is None else slots
+    free_count_out = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
+    args = (_paged("cache_len", cache_len, i32, (None,)), _paged("new_len", new_len, i32, (B,)),
+            _paged("free_pages", free_pages, i32, (None,)), _paged("free_count", free_count, i32, (1,)),
+            _paged("block_table", block_table, i32, (B, None)), _paged("kv_len", kv_len, i32, (B,)),
+            _paged("cu_q", cu_q, i32, (B + 1,)), _paged("positions", positions, i32, (T,)),
+            _paged("slots", slots, i32, (T,)), _paged("free_count_out", free_count_out, i32, (1,)))
+    d = PagedDims(B, 0, 0, 0, int(page_size), free_pages.shape[0], block_table.shape[1], T, 0)
+    stream = _paged_stream(cache_len, new_len, free_pages, free_count, block_table, kv_len, cu_q, positions, slots,
+                           free_count_out)
+    _check("paged_build_tables", lib().paged_build_tables(ctypes.byref(d), *args, stream))
+    return kv_len, cu_q, positions, slots, free_count_out
+
+
+def paged_release_pages(kv_len, keep_len, block_table, free_pages, free_count, page_size: int = PAGE_SIZE,
+                        free_count_out=None):
+    """Append the pages past keep_len [B] of kv_len [B] tokens to free_pages behind its first free_count
+    entries; returns the new count (free_count_out, which may be free_count itself)."""
+    i32 = torch.int32
+    free_count_out = torch.empty(1, dtype=i32, device=free_count.device) if free_count_out is None else free_count_out
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    args = (_paged("kv_len", kv_len, i32, (None,)), _paged("keep_len", keep_len, i32, (B,)),
+            _paged("block_table", block_table, i32, (B, None)), _paged("free_pages", free_pages, i32, (None,)),
+            _paged("free_count", free_count, i32, (1,)), _paged("free_count_out", free_count_out, i32, (1,)))
+    d = PagedDims(B, 0, 0, 0, int(page_size), free_pages.shape[0], block_table.shape[1], 1, 0)
+    stream = _paged_stream(kv_len, keep_len, block_table, free_pages, free_count, free_count_out)
+    _check("paged_release_pages", lib().paged_release_pages(ctypes.byref(d), *args, stream))
+    return free_count_out
+
+
+def _paged_rows(name: str, t, dtype, T: int, H, D: int):
+    """[T,H,D] rows whose heads are contiguous; returns (pointer, elements between tokens)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or t.shape[2] != D:
+        raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {(st, sh, sd)}")
+    if T == 1:
+        st = H * D  # a single token: whatever the stride says
+    return t.data_ptr(), st
+
+
+def paged_norm_rope_append(q, k, v, positions, slots, k_pages, v_pages, q_weight=None, k_weight=None,
+                           eps: float = 1e-6, cos_sin=None, interleaved: bool = False, q_out=None):
+    """Per-head RMS norms of q [T,Hq,D] and k [T,Hkv,D] (weights [D], each optional), rotary positions by
+    cos_sin [max_position,rope_dim] fp32 (cosines, then sines; None: no rotation), and the append: q to
+    q_out [T,Hq,D], k and v to row slots[t] of the pages [num_pages,Hkv,S,D]. Tokens with slots[t] < 0
+    are padding. q, k and v may be slices of one fused projection (heads contiguous, any token stride
+    that is a multiple of 8). Returns q_out."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor of shape [T,Hq,D]")
+    dt = q.dtype
+    T, Hq, D = q.shape
+    pk = _paged("k_pages", k_pages, dt, (None, None, None, D))
+    num_pages, Hkv, S, _ = k_pages.shape
+    pv = _paged("v_pages", v_pages, dt, (num_pages, Hkv, S, D))
+    q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device) if q_out is None else q_out
+    (aq, sq), (ak, sk), (av, sv) = (_paged_rows("q", q, dt, T, Hq, D), _paged_rows("k", k, dt, T, Hkv, D),
+                                    _paged_rows("v", v, dt, T, Hkv, D))
+    ao = _paged("q_out", q_out, dt, (T, Hq, D))
+    apos, aslot = _paged("positions", positions, torch.int32, (T,)), _paged("slots", slots, torch.int32, (T,))
+    wq = None if q_weight is None else _paged("q_weight", q_weight, dt, (D,))
+    wk = None if k_weight is None else _paged("k_weight", k_weight, dt, (D,))
+    cs, rope, most = None, 0, 0
+    if cos_sin is not None:
+        cs = _paged("cos_sin", cos_sin, torch.float32, (None, None))
+        most, rope = cos_sin.shape
+    if dt not in _PAGED_DTYPES:
+        raise ValueError(f"q must be torch.float16 or torch.bfloat16, got {dt}")
+    d = PagedDims(1, Hq, Hkv, D, S, num_pages, 1, T, _PAGED_DTYPES[dt])
+    stream = _paged_stream(q, k, v, positions, slots, k_pages, v_pages, q_weight, k_weight, cos_sin, q_out)
+    _check("paged_norm_rope_append", lib().paged_norm_rope_append(
+        ctypes.byref(d), aq, sq, ak, sk, av, sv, apos, aslot, wq, wk, eps, cs, rope, most, 1 if interleaved else 0, ao, pk,
+        pv, stream))
+    return q_out
+
+
+def gqa_paged_attn(q, k_pages, v_pages, block_table, cu_q, kv_len, scale: float, max_q_len: int, out=None,
+                   workspace=None):
+    """Attention of each request's new tokens over its pages: q [T,Hq,D] (request b owns rows
+    cu_q[b]..cu_q[b+1]-1, the last of its kv_len[b] tokens), pages [num_pages,Hkv,S,D], block_table
+    [B,max_pages]; every token attends to the tokens up to itself. max_q_len bounds the rows of a
+    request. Rows of out outside the requests' are left as they were."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor of shape [T,Hq,D]")
+    dt = q.dtype
+    T, Hq, D = q.shape
+    aq = _paged("q", q, dt, (T, Hq, D))
+    pk = _paged("k_pages", k_pages, dt, (None, None, None, D))
+    num_pages, Hkv, S, _ = k_pages.shape
+    pv = _paged("v_pages", v_pages, dt, (num_pages, Hkv, S, D))
+    tab = _paged("block_table", block_table, torch.int32, (None, None))
+    B, max_pages = block_table.shape
+    acu, alen = _paged("cu_q", cu_q, torch.int32, (B + 1,)), _paged("kv_len", kv_len, torch.int32, (B,))
+    if dt not in _PAGED_DTYPES:
+        raise ValueError(f"q must be torch.float16 or torch.bfloat16, got {dt}")
+    d = PagedDims(B, Hq, Hkv, D, S, num_pages, max_pages, T, _PAGED_DTYPES[dt])
+    out = torch.empty_like(q) if out is None else out
+    ao = _paged("out", out, dt, (T, Hq, D))
+    if workspace is None:
+        workspace = alloc_paged_workspace(d, q.device)
+    aws = _paged("workspace", workspace, torch.uint8, (None,))
+    stream = _paged_stream(q, k_pages, v_pages, block_table, cu_q, kv_len, out, workspace)
+    _check("gqa_paged_attn", lib().gqa_paged_attn(
+        ctypes.byref(d), max_q_len, aq, pk, pv, tab, acu, alen, scale, ao, aws, workspace.shape[0], stream))
+    return out

@@ -64,6 +64,25 @@ int device_state(DeviceState **out, int *dev_out) {
     return GQAQ_OK;
 }
 
+// Shape checks shared by every entry point.
+int check_dims(const gqaq_dims *d, bool quest) {
+    if (d == nullptr) return GQAQ_ERR_INVALID_ARG;
+    if (d->batch < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1 || d->max_len < 1 || d->head_dim < 1)
+        return GQAQ_ERR_INVALID_ARG;
+    if (d->num_q_heads % d->num_kv_heads != 0) return GQAQ_ERR_INVALID_ARG;
+    if (quest && d->page_size < 1) return GQAQ_ERR_INVALID_ARG;
+    const int G = d->num_q_heads / d->num_kv_heads;
+    if (G != 1 && G != 2 && G != 4 && G != 8) return GQAQ_ERR_UNSUPPORTED;
+    if (d->head_dim != 64 && d->head_dim != 128) return GQAQ_ERR_UNSUPPORTED;
+    if (quest && d->page_size != 8 && d->page_size != 16 && d->page_size != 32 && d->page_size != 64)
+        return GQAQ_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)d->batch * d->num_kv_heads * d->max_len;
+    if (rows > (int64_t)INT32_MAX - 1024) return GQAQ_ERR_UNSUPPORTED;
+    return GQAQ_OK;
+}
+
+}  // namespace
+
 int make_ctx(LaunchCtx *ctx, void *stream) {
     DeviceState *s = nullptr;
     int dev = 0;
@@ -85,27 +104,6 @@ int make_ctx(LaunchCtx *ctx, void *stream) {
     ctx->status = s->status;
     return GQAQ_OK;
 }
-
-bool aligned16(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Shape checks shared by every entry point.
-int check_dims(const gqaq_dims *d, bool quest) {
-    if (d == nullptr) return GQAQ_ERR_INVALID_ARG;
-    if (d->batch < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1 || d->max_len < 1 || d->head_dim < 1)
-        return GQAQ_ERR_INVALID_ARG;
-    if (d->num_q_heads % d->num_kv_heads != 0) return GQAQ_ERR_INVALID_ARG;
-    if (quest && d->page_size < 1) return GQAQ_ERR_INVALID_ARG;
-    const int G = d->num_q_heads / d->num_kv_heads;
-    if (G != 1 && G != 2 && G != 4 && G != 8) return GQAQ_ERR_UNSUPPORTED;
-    if (d->head_dim != 64 && d->head_dim != 128) return GQAQ_ERR_UNSUPPORTED;
-    if (quest && d->page_size != 8 && d->page_size != 16 && d->page_size != 32 && d->page_size != 64)
-        return GQAQ_ERR_UNSUPPORTED;
-    const int64_t rows = (int64_t)d->batch * d->num_kv_heads * d->max_len;
-    if (rows > (int64_t)INT32_MAX - 1024) return GQAQ_ERR_UNSUPPORTED;
-    return GQAQ_OK;
-}
-
-}  // namespace
 
 bool encode_tensor_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                           uint32_t box_cols, uint32_t box_rows, bool swizzle128) {

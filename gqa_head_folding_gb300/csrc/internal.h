@@ -13,6 +13,11 @@
 
 namespace gqaq {
 
+// Fills the launch context of the current device (abi.cu). Returns a gqaq_status.
+int make_ctx(LaunchCtx *ctx, void *stream);
+
+inline bool aligned16(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Encodes a 2-D fp16 tensor map: rows x cols (cols innermost), box of
 // box_cols x box_rows, 128-byte swizzle or none. Returns false on failure.
 bool encode_tensor_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
@@ -137,6 +142,45 @@ int launch_score_pages(const gqaq_dims *dims, const __half *q, const __half *met
                        const int *valid_len, float *scores, const LaunchCtx &ctx);
 int launch_topk_pages(const gqaq_dims *dims, const float *scores, const int *valid_len, int k,
                       int *page_idx, const LaunchCtx &ctx);
+
+// Paged caches (paged.cu): the step's plan, page release, norm + rotation + append.
+struct PagedTablesArgs {
+    const gqaq_paged_dims *dims;
+    const int *cache_len, *new_len, *free_pages, *free_count;
+    int *block_table, *kv_len, *cu_q, *positions, *slots, *free_count_out;
+};
+int launch_paged_tables(const PagedTablesArgs &a, const LaunchCtx &ctx);
+struct PagedReleaseArgs {
+    const gqaq_paged_dims *dims;
+    const int *kv_len, *keep_len, *block_table, *free_count;
+    int *free_pages, *free_count_out;
+};
+int launch_paged_release(const PagedReleaseArgs &a, const LaunchCtx &ctx);
+struct PagedAppendArgs {
+    const gqaq_paged_dims *dims;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const int *positions, *slots;
+    const void *q_weight, *k_weight;       // may be null
+    float eps;
+    const float *cos_sin;
+    int rope_dim, max_position, interleaved;
+    void *q_out, *k_pages, *v_pages;
+};
+int launch_paged_append(const PagedAppendArgs &a, const LaunchCtx &ctx);
+
+// Attention over a paged cache (paged_attn.cu).
+struct PagedAttnArgs {
+    const gqaq_paged_dims *dims;
+    int max_q_len;
+    const void *q, *k_pages, *v_pages;
+    const int *block_table, *cu_q, *kv_len;
+    float scale;
+    void *out, *workspace;
+    size_t workspace_bytes;
+};
+int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx);
+size_t paged_attn_workspace_bytes(const gqaq_paged_dims *dims, const LaunchCtx &ctx);
 
 // Largest Pmax the top-K kernel keeps in shared memory.
 constexpr int kTopkMaxPages = 32768;

@@ -80,7 +80,8 @@ enum {
     GQAQ_DEV_TIMEOUT = 1,  /* a bounded wait gave up */
     GQAQ_DEV_BAD_LEN = 2,  /* a valid_len outside [1, Lmax] was clamped */
     GQAQ_DEV_BAD_PAGE = 4, /* a page index outside [0, P) was skipped */
-    GQAQ_DEV_BAD_POS = 8   /* an append position outside [0, Lmax) was skipped */
+    GQAQ_DEV_BAD_POS = 8,  /* an append position outside [0, Lmax) was skipped */
+    GQAQ_DEV_NO_PAGES = 16 /* a request was refused: the free list holds too few pages */
 };
 
 typedef struct {
@@ -355,6 +356,143 @@ GQAQ_API size_t gqaq_prefill_workspace_bytes(const gqaq_dims *dims, int q_len);
 GQAQ_API int gqa_prefill_attn(const gqaq_dims *dims, int q_len, const gqaq_half *q, const gqaq_half *k_cache,
                               const gqaq_half *v_cache, const int32_t *start, float scale, gqaq_half *out,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged KV caches: a serving step over requests of unlike lengths.
+ *
+ * A pool of num_pages pages holds the keys, a second one the values:
+ *   k_pages, v_pages [num_pages][Hkv][S][D]   (a page of a head: S rows of D)
+ * and row b of block_table ([B][max_pages] int32) lists request b's pages in
+ * token order: token j of request b sits in row j % S of page
+ * block_table[b][j / S]. The entries from ceil(length / S) on are not read.
+ * The step's tokens lie one request behind the other in [max_tokens] rows:
+ * request b owns rows cu_q[b] .. cu_q[b+1]-1 (cu_q [B+1] int32, ascending),
+ * and rows from cu_q[B] on are padding.
+ *
+ * q, k, v, out and the pages are fp16 or bfloat16 (dims.dtype, passed as
+ * gqaq_half bits). Supported: D in {64, 128}; G in {1, 2, 4, 8}; S in
+ * {8, 16, 32, 64, 128}; B <= 8192; max_tokens <= 2^22; max_pages * S,
+ * B * max_pages and num_pages * Hkv * S below 2^31. Else GQAQ_ERR_UNSUPPORTED.
+ *
+ * As for every call, what lies on the device is checked there: lengths,
+ * positions, slots and page indices out of range are clamped or skipped and
+ * raise a flag in the device status word, and nothing outside the buffers is
+ * read or written. */
+enum { GQAQ_F16 = 0, GQAQ_BF16 = 1 };
+
+typedef struct {
+    int batch;        /* B >= 1: requests, rows of block_table */
+    int num_q_heads;  /* Hq, a multiple of Hkv */
+    int num_kv_heads; /* Hkv >= 1 */
+    int head_dim;     /* D: 64 or 128 */
+    int page_size;    /* S: 8, 16, 32, 64 or 128 tokens */
+    int num_pages;    /* pages in each pool, and entries of free_pages */
+    int max_pages;    /* columns of block_table */
+    int max_tokens;   /* T >= 1: rows of the step's token arrays */
+    int dtype;        /* GQAQ_F16 or GQAQ_BF16 */
+} gqaq_paged_dims;
+
+/* Plan a step on the GPU: from the requests' lengths, the pages they need,
+ * where every new token goes, and the prefix sums the attention takes.
+ *   cache_len  [B]  tokens in the cache before the step
+ *   new_len    [B]  tokens the step brings (0: the request rests)
+ *   free_pages [num_pages], free_count [1]: the first *free_count entries of
+ *              free_pages are the free pages; pages are taken from their end
+ *   block_table [B][max_pages] in/out: row b's first ceil(cache_len[b] / S)
+ *              entries are read, the entries of its new pages written
+ *   kv_len     [B]  out: cache_len + new_len, or 0 for a refused request
+ *   cu_q       [B+1] out: prefix sums of new_len
+ *   positions, slots [T] out: for the token in row t its position in its
+ *              request, and page * S + row of its place in the pool; 0 and -1
+ *              in padding rows and for refused requests
+ *   free_count_out [1] out: pages left (may be free_count itself)
+ * Requests are served in order, each wholly or not at all: one whose pages
+ * (with those of all requests before it) exceed the free ones is refused and
+ * raises GQAQ_DEV_NO_PAGES; its row of block_table keeps what it held.
+ * Negative lengths, and lengths past max_pages * S, refuse the request with
+ * GQAQ_DEV_BAD_LEN (a negative new_len counts as no rows); rows past T do so
+ * with GQAQ_DEV_BAD_POS. A page index outside [0, num_pages), in the table or
+ * on the free list, raises GQAQ_DEV_BAD_PAGE and gives its tokens slot -1.
+ * The outputs (but free_count_out) must not overlap the inputs. Head counts,
+ * D and dtype of dims are not used. Every array holds int32. */
+GQAQ_API int paged_build_tables(const gqaq_paged_dims *dims, const int32_t *cache_len, const int32_t *new_len,
+                                const int32_t *free_pages, const int32_t *free_count, int32_t *block_table,
+                                int32_t *kv_len, int32_t *cu_q, int32_t *positions, int32_t *slots,
+                                int32_t *free_count_out, void *stream);
+
+/* Return pages to the free list: request b keeps its first keep_len[b] of
+ * kv_len[b] tokens (0: it has ended; less than kv_len: a rejected tail), and
+ * its pages from ceil(keep_len / S) to ceil(kv_len / S) are appended to
+ * free_pages behind the first *free_count entries, in order of (request,
+ * page). block_table is not changed: its entries past the kept length are no
+ * longer the request's. free_count_out [1] (may be free_count itself) becomes
+ * the new count. A request with keep_len outside [0, kv_len] or kv_len
+ * outside [0, max_pages * S] keeps all its pages and raises
+ * GQAQ_DEV_BAD_LEN; pages that would pass the end of free_pages are dropped
+ * and raise GQAQ_DEV_BAD_LEN. Uses B, S, num_pages and max_pages of dims. */
+GQAQ_API int paged_release_pages(const gqaq_paged_dims *dims, const int32_t *kv_len, const int32_t *keep_len,
+                                 const int32_t *block_table, int32_t *free_pages, const int32_t *free_count,
+                                 int32_t *free_count_out, void *stream);
+
+/* What stands between a layer's projection and its attention, in one pass:
+ * per-head RMS norms of q and k, the rotary position, and the append of the
+ * step's k and v rows to the pages. For token t and head h, in fp32:
+ *   y = x * rsqrt(mean_i(x_i^2) + eps) * weight   (weight NULL: y = x)
+ * then channels 0 .. rope_dim-1 of y turn by the angles of positions[t]:
+ *   interleaved = 0: pairs (i, i + rope_dim/2); 1: pairs (2i, 2i+1)
+ *   (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i)
+ * with cos_sin [max_position][rope_dim] fp32, the rope_dim/2 cosines of a
+ * position, then its sines. Results are rounded once. q goes to q_out
+ * [T][Hq][D], k to row slots[t] of k_pages; v's row is copied to v_pages.
+ *   q [T][Hq][D], k, v [T][Hkv][D]: heads contiguous, tokens q_stride,
+ *   k_stride, v_stride elements apart (multiples of 8), so the slices of one
+ *   fused projection are taken as they are. q_out may be q itself when
+ *   q_stride = Hq*D.
+ * q_weight / k_weight [D] (dtype of q; each may be NULL), rope_dim a multiple
+ * of 16 in [0, D]; cos_sin may be NULL when rope_dim = 0.
+ * A token with a negative slot is padding: nothing of it is read or written.
+ * A slot at or past num_pages * S raises GQAQ_DEV_BAD_PAGE and a position
+ * outside [0, max_position) (with rope_dim > 0) GQAQ_DEV_BAD_POS; the token
+ * is then skipped like padding. Slots >= 0 must be distinct: of two tokens
+ * with one slot either's row, or a mixture, stays. Uses Hq, Hkv, D, S,
+ * num_pages, max_tokens and dtype of dims. */
+GQAQ_API int paged_norm_rope_append(const gqaq_paged_dims *dims, const gqaq_half *q, int64_t q_stride,
+                                    const gqaq_half *k, int64_t k_stride, const gqaq_half *v, int64_t v_stride,
+                                    const int32_t *positions, const int32_t *slots, const gqaq_half *q_weight,
+                                    const gqaq_half *k_weight, float eps, const float *cos_sin, int rope_dim,
+                                    int max_position, int interleaved, gqaq_half *q_out, gqaq_half *k_pages,
+                                    gqaq_half *v_pages, void *stream);
+
+/* Bytes of workspace gqa_paged_attn needs on the current device. Depends on
+ * D and the SM count only; 0 when dims are invalid or unsupported. Zero-fill
+ * it once; every call leaves its counters at zero. */
+GQAQ_API size_t gqaq_paged_workspace_bytes(const gqaq_paged_dims *dims);
+
+/* Attention of each request's new tokens over its pages: one token, a few
+ * drafted ones, a chunk of a prompt, or any mixture in one call.
+ * q, out [T][Hq][D]. Request b has q_len = cu_q[b+1] - cu_q[b] new tokens,
+ * the last q_len of its kv_len[b] tokens (their keys and values are in the
+ * pages). Token i of them attends to tokens 0 .. kv_len - q_len + i:
+ *   out = softmax(scale * q . k) v   per head, KV head h / G,
+ * fp32 scores, sums and accumulation, one rounding of each probability to
+ * the dtype and one of out. A token whose position is negative (kv_len <
+ * q_len, as 0 for a refused request) has nothing to attend to: its out is 0.
+ * Rows outside [cu_q[0], cu_q[B]) of out are left as they were. Stale rows of
+ * a page past kv_len may hold anything, NaN included; the values (v) of the
+ * request's own tokens must be finite, or a token may see those of a later
+ * token of its chunk.
+ * max_q_len: the host's bound on q_len (it selects the kernel). A request
+ * with more raises GQAQ_DEV_BAD_LEN and only its first max_q_len tokens are
+ * computed. kv_len outside [0, max_pages * S] is clamped and raises
+ * GQAQ_DEV_BAD_LEN; a cu_q entry that descends or leaves [0, T] is clamped
+ * and raises GQAQ_DEV_BAD_POS; a page index outside [0, num_pages) raises
+ * GQAQ_DEV_BAD_PAGE, and its page reads as zeros.
+ * workspace: >= gqaq_paged_workspace_bytes(dims), zero-filled before its
+ * first use. Two calls that overlap on the GPU must not share it. */
+GQAQ_API int gqa_paged_attn(const gqaq_paged_dims *dims, int max_q_len, const gqaq_half *q, const gqaq_half *k_pages,
+                            const gqaq_half *v_pages, const int32_t *block_table, const int32_t *cu_q,
+                            const int32_t *kv_len, float scale, gqaq_half *out, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 /* Human-readable name of a gqaq_status value (static string). */
 GQAQ_API const char *gqaq_status_string(int status);
