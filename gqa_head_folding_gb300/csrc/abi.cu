@@ -168,6 +168,19 @@ bool encode_tensor_map_kpage(CUtensorMap *map, const void *base, uint64_t rows, 
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tensor_map_heads(CUtensorMap *map, const void *base, uint64_t tokens, uint64_t heads, uint64_t cols,
+                             uint32_t box_heads, uint32_t box_tokens) {
+    if (cols % 64 != 0 || !encode_tensor_map_2d(map, base, tokens * heads, cols, 64, 1, true)) return false;  // loads g_encode
+    const cuuint64_t dims[3] = {cols, heads, tokens};
+    const cuuint64_t strides[2] = {cols * 2, heads * cols * 2};
+    const cuuint32_t box[3] = {64, box_heads, box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace gqaq
 
 using namespace gqaq;

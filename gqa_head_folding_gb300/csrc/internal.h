@@ -26,6 +26,9 @@ bool encode_tensor_map_2d(CUtensorMap *map, const void *base, uint64_t rows, uin
 // 128-byte swizzle: one TMA load brings box_rows whole rows (all their
 // 128-byte column blocks, interleaved row by row). cols: a multiple of 64.
 bool encode_tensor_map_kpage(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// Rows of tokens [tokens][heads][cols] of 16 bits, box [box_tokens][box_heads][64], 128-byte swizzle.
+bool encode_tensor_map_heads(CUtensorMap *map, const void *base, uint64_t tokens, uint64_t heads, uint64_t cols,
+                             uint32_t box_heads, uint32_t box_tokens);
 // fp32 matrix [rows][cols] (INT4 scale rows, cols * 4 a multiple of 16), box [1][box_cols].
 bool encode_tensor_map_f32_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols);
 // Byte matrix [rows][cols] (E4M3 codes), box [box_rows][cols], swizzle 0, 64 or 128 bytes.
@@ -181,6 +184,12 @@ struct PagedAttnArgs {
 };
 int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx);
 size_t paged_attn_workspace_bytes(const gqaq_paged_dims *dims, const LaunchCtx &ctx);
+// Its kernels. The workspace holds arrival counters (one word per CTA, zero
+// between calls) in its first kPagedCountBytes, then the partials.
+constexpr size_t kPagedCountBytes = 4096;
+int paged_tc_grid(const LaunchCtx &ctx);
+int launch_paged_tc(const PagedAttnArgs &a, const LaunchCtx &ctx);
+size_t paged_tc_workspace_bytes(const gqaq_paged_dims *dims, const LaunchCtx &ctx);
 
 // Largest Pmax the top-K kernel keeps in shared memory.
 constexpr int kTopkMaxPages = 32768;

@@ -137,10 +137,11 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(const gqaq_paged_dims *, const LaunchCtx &) { return 256; }
+size_t paged_attn_workspace_bytes(const gqaq_paged_dims *d, const LaunchCtx &ctx) { return paged_tc_workspace_bytes(d, ctx); }
 
 int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (a.workspace_bytes < paged_attn_workspace_bytes(a.dims, ctx)) return GQAQ_ERR_WORKSPACE;
+    if ((int64_t)a.max_q_len * (a.dims->num_q_heads / a.dims->num_kv_heads) > 8) return launch_paged_tc(a, ctx);
     if (a.dims->dtype == GQAQ_BF16) return a.dims->head_dim == 128 ? launch_t<128, true>(a, ctx) : launch_t<64, true>(a, ctx);
     return a.dims->head_dim == 128 ? launch_t<128, false>(a, ctx) : launch_t<64, false>(a, ctx);
 }

@@ -1,0 +1,249 @@
+// paged_sched.cuh -- how the paged attention kernels share out a ragged step.
+//
+// An item is (request, KV head, block of TB tokens); the G query heads of the
+// KV head and the block's tokens form its rows, token outer: row r is token
+// r / G, head r % G. An item's context is cut into tiles of 128 tokens, up to
+// its last row's position. The tiles of all items, in the order (request, KV
+// head, block, tile), are split into equal contiguous ranges, one per CTA, so
+// a batch of unlike lengths loads all SMs alike; consecutive CTAs work on the
+// same keys, which the L2 then serves. An item cut by a range boundary is
+// merged by the CTA that finishes last.
+#pragma once
+
+#include "internal.h"
+
+namespace gqaq {
+
+constexpr int kPagedTileLog = 7, kPagedTile = 1 << kPagedTileLog;
+
+struct PagedWorkParams {
+    const int *table, *cu_q, *kv_len;
+    int B, T, Hkv, max_q;
+    int shift;             // log2 of the page size
+    int tbs;               // log2 of TB, the tokens per block
+    int num_pages, max_pages;
+    int64_t room;          // max_pages * page size
+};
+
+inline void fill_paged_work(const PagedAttnArgs &a, int tbs, PagedWorkParams &w) {
+    const gqaq_paged_dims &d = *a.dims;
+    w.table = a.block_table;
+    w.cu_q = a.cu_q;
+    w.kv_len = a.kv_len;
+    w.B = d.batch;
+    w.T = d.max_tokens;
+    w.Hkv = d.num_kv_heads;
+    w.max_q = a.max_q_len;
+    w.tbs = tbs;
+    w.shift = 0;
+    while ((1 << w.shift) < d.page_size) ++w.shift;
+    w.num_pages = d.num_pages;
+    w.max_pages = d.max_pages;
+    w.room = (int64_t)d.max_pages * d.page_size;
+}
+
+// One request as the kernels see it, clamped to what the buffers hold.
+struct PagedSeq {
+    int q0;     // first row of its tokens
+    int m;      // tokens computed: min(q_len, max_q)
+    int start;  // position of its first new token (negative: tokens without a place)
+    int len;    // tokens in the cache
+    int flags;
+    __device__ __forceinline__ void load(const PagedWorkParams &p, int b) {
+        const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], raw = p.kv_len[b];
+        flags = 0;
+        q0 = min(max(c0, 0), p.T);
+        const int q1 = min(max(c1, q0), p.T);
+        if (q0 != c0 || q1 != c1) flags |= GQAQ_DEV_BAD_POS;
+        len = (int)min((int64_t)max(raw, 0), p.room);
+        if (len != raw) flags |= GQAQ_DEV_BAD_LEN;
+        const int n = q1 - q0;
+        m = min(n, p.max_q);
+        if (m != n) flags |= GQAQ_DEV_BAD_LEN;
+        start = len - n;
+    }
+};
+
+// Tiles of block rb: those up to the position of its last token.
+__device__ __forceinline__ int block_tiles(const PagedSeq &s, int rb, int tbs) {
+    const int64_t end = (int64_t)s.start + min((int64_t)(rb + 1) << tbs, (int64_t)s.m);
+    return end > 0 ? (int)((end + kPagedTile - 1) >> kPagedTileLog) : 0;
+}
+
+// sum_{i=1}^{n} ceil(i / 2^k)
+__device__ __forceinline__ int64_t sum_ceil(int64_t n, int k) {
+    const int64_t q = n >> k, r = n - (q << k);
+    return ((q * (q + 1) / 2) << k) + r * (q + 1);
+}
+
+// Tiles of the first rb (whole) blocks. A block's tiles are
+// ceil((start + (k + 1) TB) / 128): an arithmetic series when TB is a multiple
+// of the tile, else a series in units of TB that rises every 128 / TB blocks.
+__device__ __forceinline__ int64_t tiles_before(const PagedSeq &s, int64_t rb, int tbs) {
+    if (rb <= 0) return 0;
+    int64_t a = (int64_t)s.start + (1ll << tbs), n = rb;
+    if (a <= 0) {  // blocks that end before position zero have no tile
+        const int64_t skip = (-a >> tbs) + 1;
+        if (skip >= n) return 0;
+        a += skip << tbs;
+        n -= skip;
+    }
+    if (tbs >= kPagedTileLog)
+        return n * ((a + kPagedTile - 1) >> kPagedTileLog) + ((n * (n - 1) / 2) << (tbs - kPagedTileLog));
+    const int64_t u = (a + (1ll << tbs) - 1) >> tbs;
+    return sum_ceil(u + n - 1, kPagedTileLog - tbs) - sum_ceil(u - 1, kPagedTileLog - tbs);
+}
+
+__device__ __forceinline__ int64_t head_tiles(const PagedSeq &s, int tbs) {
+    if (s.m <= 0) return 0;
+    const int last = (s.m - 1) >> tbs;
+    return tiles_before(s, last, tbs) + block_tiles(s, last, tbs);
+}
+
+// What a CTA knows of its range.
+struct PagedSched {
+    int64_t T, t_begin, t_end;  // tiles of all items; this CTA's range
+    int64_t off_b;              // tile offset of request b
+    int b;                      // request of the range's first tile
+    int grid;                   // CTAs with work
+    int abort;
+    int last;                   // this CTA arrived last at the item
+};
+
+// A CTA's place in its range: one item (segment) after the other.
+struct PagedWalk {
+    PagedSeq s;
+    int b, kv, rb, local, tiles;  // tile `local` of the item's `tiles`
+    int64_t off, remaining;       // tile offset of the item
+    bool first;
+    __device__ __forceinline__ void init(const PagedWorkParams &p, const PagedSched &w) {
+        b = w.b;
+        s.load(p, b);
+        const int64_t head = head_tiles(s, p.tbs), rel = w.t_begin - w.off_b;
+        kv = (int)(rel / head);
+        const int64_t in_head = rel - kv * head;
+        int lo = 0, hi = ((s.m - 1) >> p.tbs) + 1;  // the last block that begins at or before in_head
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tiles_before(s, mid, p.tbs) <= in_head) lo = mid; else hi = mid;
+        }
+        rb = lo;
+        const int64_t before = tiles_before(s, rb, p.tbs);
+        local = (int)(in_head - before);
+        tiles = block_tiles(s, rb, p.tbs);
+        off = w.off_b + kv * head + before;
+        remaining = w.t_end - w.t_begin;
+        first = true;
+    }
+    __device__ __forceinline__ int seg_len() const {
+        const int64_t r = tiles - local;
+        return (int)(r < remaining ? r : remaining);
+    }
+    __device__ __forceinline__ bool whole() const { return local == 0 && tiles <= remaining; }
+    // Move past a segment of n tiles; false when the range is done.
+    __device__ __forceinline__ bool next(int n, const PagedWorkParams &p) {
+        remaining -= n;
+        first = false;
+        if (remaining <= 0) return false;
+        off += tiles;
+        local = 0;
+        do {
+            if (((int64_t)(rb + 1) << p.tbs) < s.m) {
+                ++rb;
+            } else {
+                rb = 0;
+                if (++kv == p.Hkv) {
+                    kv = 0;
+                    do {
+                        if (++b >= p.B) return false;
+                        s.load(p, b);
+                    } while (s.m <= 0 || s.start + s.m <= 0);
+                }
+            }
+            tiles = block_tiles(s, rb, p.tbs);
+        } while (tiles == 0);
+        return true;
+    }
+};
+
+// Threads 0 .. 255 (whole CTA must call; it has __syncthreads): the tiles of
+// all items, and the request that holds the range's first tile. scratch: 8
+// words of 64 bits. min_tiles: a small step keeps this many tiles per CTA.
+__device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSched *sched, int64_t *scratch, int min_tiles) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + 255) / 256;
+    int64_t mine = 0, incl = 0;
+    int b0 = 0, b1 = 0;
+    if (tid < 256) {
+        b0 = min(tid * per, p.B);
+        b1 = min(b0 + per, p.B);
+        for (int b = b0; b < b1; ++b) {
+            PagedSeq s;
+            s.load(p, b);
+            mine += p.Hkv * head_tiles(s, p.tbs);
+        }
+        incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) scratch[warp] = incl;
+    }
+    __syncthreads();
+    if (tid < 256) {
+        int64_t total = 0, base = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) base += scratch[w];
+            total += scratch[w];
+        }
+        const int64_t want = (total + min_tiles - 1) / min_tiles;
+        const int grid = want < (int64_t)gridDim.x ? (int)want : (int)gridDim.x;
+        int64_t tb = 0, te = 0;
+        if ((int)blockIdx.x < grid) {
+            tb = tile_begin(blockIdx.x, total, grid);
+            te = tile_begin(blockIdx.x + 1, total, grid);
+        }
+        int64_t off = base + incl - mine;
+        if (tid == 0) {
+            sched->T = total;
+            sched->grid = grid;
+            sched->t_begin = tb;
+            sched->t_end = te;
+            sched->abort = 0;
+            sched->last = 0;
+        }
+        if (tb < te && off <= tb && tb < off + mine) {  // one thread's requests hold tile tb
+            for (int b = b0; b < b1; ++b) {
+                PagedSeq s;
+                s.load(p, b);
+                const int64_t n = p.Hkv * head_tiles(s, p.tbs);
+                if (tb < off + n) {
+                    sched->b = b;
+                    sched->off_b = off;
+                    break;
+                }
+                off += n;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// Threads 0 .. nthreads-1: flags of bad lengths, and zeros for the tokens that
+// have nothing to attend to (their items have no tile). Request b is CTA
+// b % gridDim.x's. row_words: 16-byte words of a token's output (Hq * D * 2 / 16).
+__device__ __forceinline__ void paged_zero_rows(const PagedWorkParams &p, uint4 *out, int row_words, int *status, int nthreads) {
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        PagedSeq s;
+        s.load(p, b);
+        if (threadIdx.x == 0 && s.flags) raise_flag(status, s.flags);
+        if (s.start >= 0) continue;
+        const int64_t n = (int64_t)min(s.m, -s.start) * row_words;
+        uint4 *o = out + (int64_t)s.q0 * row_words;
+        for (int64_t e = threadIdx.x; e < n; e += nthreads) o[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+}  // namespace gqaq
