@@ -12,14 +12,16 @@
 // Kernel shape (one persistent CTA per SM, one launch):
 //  - an item is 256 rows (two tiles of 128) of one (request, KV head), see
 //    paged_sched.cuh; a CTA walks the tiles of its range.
-//  - warp 8 loads Q and the K tiles, warp 10 the V tiles: one 64-channel box
+//  - warp 16 loads Q and the K tiles, warp 18 the V tiles: one 64-channel box
 //    of S rows per page and column block, so a tile of 128 tokens is gathered
 //    from its pages in the order of the table; each tile lands in a ring of
 //    its own. Boxes of pages past the request read out of bounds: zeros.
-//  - warp 9 issues the MMAs: S = Q K^T (M 128, N 128) and O += P V (A = P from
+//  - warp 17 issues the MMAs: S = Q K^T (M 128, N 128) and O += P V (A = P from
 //    tensor memory, B = V, N = D).
-//  - warps 0-3 and 4-7 are two softmax groups, a thread per row, each with its
-//    own S and O in tensor memory (S0, S1, O0, O1: 512 columns at D = 128).
+//  - warps 0-7 and 8-15 are two softmax groups, two threads per row (64 tokens
+//    each: twice the warps halve the time from S to P, which the tensor core
+//    waits for), each group with its own S and O in tensor memory (S0, S1, O0,
+//    O1: 512 columns at D = 128).
 //    An item of two row tiles gives each group one of them; every K / V tile
 //    then serves 256 rows. An item of one row tile gives both groups the same
 //    rows and every other K / V tile, and they merge at its end. Either way
@@ -37,7 +39,7 @@ namespace {
 
 template <int D>
 struct PtcCfg {
-    static constexpr int THREADS = 352;              // 8 softmax warps, K, MMA, V
+    static constexpr int THREADS = 608;              // 16 softmax warps, K, MMA, V
     static constexpr int RB = 256;                   // rows per item
     static constexpr int KH = D / 64;                // 64-channel blocks
     static constexpr int BLK = 128 * 128;            // one block of 128 rows
@@ -53,8 +55,9 @@ struct PtcCfg {
 };
 
 constexpr int kMinTiles = 2;        // tiles per CTA below which a small step uses fewer CTAs
-constexpr float kSumLimit = 32768.f;
-constexpr float kRefDrop = 6.f;     // the reference's distance under the maximum that sets it (log2)
+constexpr float kSumLimit = 32768.f;  // of 64 P: above it some P passes 2^9
+constexpr float kRefMove = 9.f;       // log2 of the P that moves a row's reference
+constexpr float kRefDrop = 6.f;       // the new reference's distance under the row's maximum
 
 struct PtcParams {
     PagedWorkParams w;
@@ -89,6 +92,66 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// True on the 64 threads of barrier `id` when any of them passed true.
+__device__ __forceinline__ bool pair_any(int id, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// One product of a converged warp: its elected lane issues four K-steps (always
+// the same lane, so that its commits cover them). With the operands in
+// warp-uniform control flow the descriptors stay in uniform registers; issued
+// from a one-lane branch each MMA took about 100 cycles, twice its work.
+// Both operands from shared memory, 32 bytes (two descriptor units) per step.
+__device__ __forceinline__ void warp_mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred q, p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from tensor memory (8 columns per step), B 16 rows of 128 bytes per step.
+__device__ __forceinline__ void warp_mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred q, p, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -108,8 +171,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     uint8_t *sq = smem;                        // two Q tiles
     uint8_t *sk = sq + 2 * C::TILE;
     uint8_t *sv = sk + C::NK * C::TILE;
-    float2 *xchg = reinterpret_cast<float2 *>(sv + C::NV * C::TILE);  // [128]
-    uint64_t *kfull = reinterpret_cast<uint64_t *>(xchg + 128);
+    float *xchg = reinterpret_cast<float *>(sv + C::NV * C::TILE);  // [256]
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(xchg + 256);
     uint64_t *kempty = kfull + C::NK;
     uint64_t *vfull = kempty + C::NK;
     uint64_t *vempty = vfull + C::NV;
@@ -123,11 +186,11 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     int64_t *scratch = reinterpret_cast<int64_t *>(drain + 1);  // [8]
     PagedSched *sched = reinterpret_cast<PagedSched *>(scratch + 8);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sched + 1);
-    static_assert(128 * 8 + (2 * C::NK + 2 * C::NV + 10 + 8) * 8 + sizeof(PagedSched) + 8 <= C::MISC, "misc region");
+    static_assert(256 * 4 + (2 * C::NK + 2 * C::NV + 10 + 8) * 8 + sizeof(PagedSched) + 8 <= C::MISC, "misc region");
     volatile int *abort_flag = &sched->abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 8 && lane == 0) {
+    if (warp == 16 && lane == 0) {
         for (int s = 0; s < C::NK; ++s) {
             mbar_init(smem_u32(&kfull[s]), 1);
             mbar_init(smem_u32(&kempty[s]), 1);
@@ -140,17 +203,17 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
         mbar_init(smem_u32(qempty), 1);
         for (int g = 0; g < 2; ++g) {
             mbar_init(smem_u32(&s_ready[g]), 1);
-            mbar_init(smem_u32(&p_ready[g]), 4);  // the group's four warps
+            mbar_init(smem_u32(&p_ready[g]), 8);  // the group's warps
             mbar_init(smem_u32(&o_done[g]), 1);
         }
-        mbar_init(smem_u32(o_free), 8);
+        mbar_init(smem_u32(o_free), 16);
         mbar_init(smem_u32(drain), 1);
         fence_mbar_init();
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
-    if (warp == 9) {
+    if (warp == 17) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -159,18 +222,18 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     paged_schedule(p.w, sched, scratch, kMinTiles);
     tc_fence_after();
     const uint32_t tbase = *tslot;
-    if (warp < 8) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 256);
+    if (warp < 16) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 512);
     const bool work = sched->t_begin < sched->t_end;
 
     if (work) {
         const int TB = C::RB >> p.gshift;  // tokens of an item
         PagedWalk w;
         w.init(p.w, *sched);
-        if ((warp == 8 || warp == 10) && !p.test_stall) {
+        if ((warp == 16 || warp == 18) && !p.test_stall) {
             // --------------------------------------------------------------
-            // Loaders: K (and Q) in warp 8, V in warp 10. A lane per page.
+            // Loaders: K (and Q) in warp 16, V in warp 18. A lane per page.
             // --------------------------------------------------------------
-            const bool is_k = warp == 8;
+            const bool is_k = warp == 16;
             const int NS = is_k ? C::NK : C::NV;
             uint64_t *full = is_k ? kfull : vfull, *empty = is_k ? kempty : vempty;
             const CUtensorMap *map = is_k ? &kmap : &vmap;
@@ -240,86 +303,112 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     for (int it = seg > 1 ? seg - 1 : 0; it <= seg; ++it)  // Q of this segment, if it was asked for
                         mbar_wait(smem_u32(qfull), (uint32_t)it & 1u, p.timeout_ns / 8, nullptr);
             }
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 17) {
             // --------------------------------------------------------------
-            // MMA issuer (one thread). Products alternate between the groups:
-            // event e is tile e / 2 of group e % 2 (two row tiles), or tile e
-            // for group e % 2 (one). S(e + 2) follows PV(e), which frees its
-            // tensor memory: the core runs one thread's MMAs in order.
+            // MMA issuer (the whole warp walks, one elected lane issues).
+            // Products alternate between the groups: event e is tile e / 2 of
+            // group e % 2 (two row tiles), or tile e for group e % 2 (one).
+            // S(e + 2) follows PV(e), which frees its tensor memory: the core
+            // runs one thread's MMAs in order.
             // --------------------------------------------------------------
             constexpr uint32_t IDESC_S = umma_idesc(128, 128, 0, BF16);
             constexpr uint32_t IDESC_O = umma_idesc(128, D, 1, BF16);
             const uint64_t qdesc0 = umma_desc(smem_u32(sq), 16);
             const uint64_t kdesc0 = umma_desc(smem_u32(sk), 16);
             const uint64_t vdesc0 = umma_desc(smem_u32(sv), C::BLK);
-            int kc = 0;             // K / V tiles before this segment
-            int seg = 0;
-            uint32_t pc = 0;        // parity of the next P of each group (bits 0, 1)
-            bool ok = true;
+            int ks = 0, vs = 0;             // ring slots and their phases
+            uint32_t kp = 0, vp = 0;
+            uint32_t pp = 0;                // phases of p_ready (bits 0, 1)
+            uint32_t sp = 0;                // phase of the segment's barriers
+            bool first_seg = true, ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+                return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.timeout_ns, abort_flag)) != 0;
+            };
+            auto segment = [&](auto dual_c, int ne) {
+                constexpr bool DUAL = decltype(dual_c)::value;
+                auto issue_s = [&](int e) {
+                    const int x = e & 1;
+                    if (!DUAL || x == 0) ok = wait(&kfull[ks], kp);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t qd = qdesc0 + (uint64_t)(DUAL && x ? C::TILE >> 4 : 0);
+                    const uint64_t kd = kdesc0 + (uint64_t)(ks * (C::TILE >> 4));
+                    const uint32_t sd = tbase + C::S_COL + 128u * (uint32_t)x;
+#pragma unroll
+                    for (int kh = 0; kh < C::KH; ++kh)
+                        warp_mma_ss4(sd, qd + (uint64_t)(kh * (C::BLK >> 4)), kd + (uint64_t)(kh * (C::BLK >> 4)), IDESC_S, kh > 0);
+                    warp_commit(smem_u32(&s_ready[x]));
+                    if (!DUAL || x == 1) {
+                        warp_commit(smem_u32(&kempty[ks]));
+                        if (++ks == C::NK) {
+                            ks = 0;
+                            kp ^= 1u;
+                        }
+                    }
+                    if (e == ne - 1) warp_commit(smem_u32(qempty));
+                };
+                issue_s(0);
+                if (ok && ne > 1) issue_s(1);
+#pragma unroll 1
+                for (int e = 0; e < ne && ok; ++e) {
+                    const int x = e & 1;
+                    if (!DUAL || x == 0) ok = wait(&vfull[vs], vp);
+                    if (e == 0 && !first_seg) ok = ok && wait(o_free, sp ^ 1u);  // the last segment's O has been read
+                    ok = ok && wait(&p_ready[x], (pp >> x) & 1u);
+                    if (!ok) break;
+                    pp ^= 1u << x;
+                    tc_fence_after();
+                    const uint64_t vd = vdesc0 + (uint64_t)(vs * (C::TILE >> 4));
+                    const uint32_t od = tbase + C::O_COL + 128u * (uint32_t)x, pd = tbase + C::S_COL + 128u * (uint32_t)x;
+                    warp_mma_ts4(od, pd, vd, IDESC_O, e > 1);              // P of tokens 0-63: columns 0-31
+                    warp_mma_ts4(od, pd + 64u, vd + 512u, IDESC_O, 1);     // of tokens 64-127: columns 64-95
+                    if (!DUAL || x == 1) {
+                        warp_commit(smem_u32(&vempty[vs]));
+                        if (++vs == C::NV) {
+                            vs = 0;
+                            vp ^= 1u;
+                        }
+                    }
+                    if (e + 2 >= ne) warp_commit(smem_u32(&o_done[x]));
+                    if (e + 2 < ne) issue_s(e + 2);
+                }
+            };
             do {
                 const int n = w.seg_len();
                 const int rows = min(TB, w.s.m - w.rb * TB) * p.G;
-                const bool dual = rows > 128;
-                const int ne = dual ? 2 * n : n;
-                ok = mbar_wait(smem_u32(qfull), (uint32_t)seg & 1u, p.timeout_ns, abort_flag);
-                auto issue_s = [&](int e) {
-                    const int x = e & 1, j = kc + (dual ? e >> 1 : e), s = j % C::NK;
-                    if (!dual || x == 0) ok = ok && mbar_wait(smem_u32(&kfull[s]), (uint32_t)(j / C::NK) & 1u, p.timeout_ns, abort_flag);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t qd = qdesc0 + (uint64_t)(dual && x ? C::TILE >> 4 : 0);
-                    const uint64_t kd = kdesc0 + (uint64_t)((s * C::TILE) >> 4);
-                    const uint32_t sd = tbase + C::S_COL + 128u * (uint32_t)x;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t o = (uint64_t)(((ks >> 2) * C::BLK + (ks & 3) * 32) >> 4);
-                        umma_ss(sd, qd + o, kd + o, IDESC_S, ks > 0);
-                    }
-                    umma_commit(smem_u32(&s_ready[x]));
-                    if (!dual || x == 1) umma_commit(smem_u32(&kempty[s]));
-                    if (e == ne - 1) umma_commit(smem_u32(qempty));
-                };
-                issue_s(0);
-                if (ne > 1) issue_s(1);
-                for (int e = 0; e < ne && ok; ++e) {
-                    const int x = e & 1, j = kc + (dual ? e >> 1 : e), s = j % C::NV;
-                    ok = mbar_wait(smem_u32(&p_ready[x]), (pc >> x) & 1u, p.timeout_ns, abort_flag);
-                    pc ^= 1u << x;
-                    if (e == 0 && seg > 0)  // the last segment's O has been read
-                        ok = ok && mbar_wait(smem_u32(o_free), (uint32_t)(seg - 1) & 1u, p.timeout_ns, abort_flag);
-                    if (!dual || x == 0) ok = ok && mbar_wait(smem_u32(&vfull[s]), (uint32_t)(j / C::NV) & 1u, p.timeout_ns, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = vdesc0 + (uint64_t)((s * C::TILE) >> 4);
-                    const uint32_t od = tbase + C::O_COL + 128u * (uint32_t)x, pd = tbase + C::S_COL + 128u * (uint32_t)x;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(od, pd + 8u * kk, vd + (uint64_t)((kk * 16 * 128) >> 4), IDESC_O, (e > 1 || kk > 0) ? 1 : 0);
-                    if (!dual || x == 1) umma_commit(smem_u32(&vempty[s]));
-                    if (e + 2 >= ne) umma_commit(smem_u32(&o_done[x]));
-                    if (e + 2 < ne) issue_s(e + 2);
+                ok = wait(qfull, sp);
+                if (ok) {
+                    if (rows > 128) segment(std::true_type(), 2 * n);
+                    else segment(std::false_type(), n);
                 }
-                kc += n;
-                ++seg;
+                sp ^= 1u;
+                first_seg = false;
             } while (ok && w.next(w.seg_len(), p.w));
-            if (!ok) {
+            if (!ok && lane == 0) {
                 raise_flag(p.status, GQAQ_DEV_TIMEOUT);
                 *abort_flag = 1;
             }
-            umma_commit(smem_u32(drain));  // every issued MMA completes before TMEM is released
+            __syncwarp();
+            warp_commit(smem_u32(drain));  // every issued MMA completes before TMEM is released
             mbar_wait(smem_u32(drain), 0u, p.timeout_ns, nullptr);
-        } else if (warp < 8) {
+            __syncwarp();
+        } else if (warp < 16) {
             // --------------------------------------------------------------
-            // Softmax groups: thread = row
+            // Softmax groups: two threads per row, tokens 64 h .. 64 h + 63 of
+            // a tile each. They share the row's reference and agree on moving
+            // it (a predicate over the pair of warps); each keeps its sum.
             // --------------------------------------------------------------
-            const int g = warp >> 2, row = threadIdx.x & 127, tid = threadIdx.x;
+            const int g = warp >> 3, h = (warp >> 2) & 1, row = (warp & 3) * 32 + lane, tid = threadIdx.x;
+            const int pair_bar = 2 + g * 4 + (warp & 3);
             const uint32_t tlane = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-            const uint32_t scol = tlane + C::S_COL + 128u * (uint32_t)g;
-            const uint32_t ocol = tlane + C::O_COL + 128u * (uint32_t)g;
+            const uint32_t scol = tlane + C::S_COL + 128u * (uint32_t)g + 64u * (uint32_t)h;
+            const uint32_t ocol = tlane + C::O_COL + 128u * (uint32_t)g + (uint32_t)(h * (D / 2));  // the half it rescales
             const bool neg = !(p.scale_log2 > 0.f);  // a positive scale folds into the exponent
             const float mul = neg ? 1.f : p.scale_log2;
-            int sc = 0, oc = 0;  // S tiles and finished segments of this group
-            int vc = 0;          // V tiles before this segment
+            uint32_t sph = 0, oph = 0;  // phases of s_ready and o_done
+            int vs = 0;                 // V slot of the segment's first tile, and its phase
+            uint32_t vp = 0;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 bool r = true;
@@ -344,25 +433,24 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const int lim_lo = pos0 + ((r0 + (warp & 3) * 32) >> p.gshift);  // the warp's least
                 float ref = -INFINITY, l = 0.f;
                 for (int k = 0; k < nx; ++k) {
-                    const int jj = dual ? k : 2 * k + g;  // tile within the segment
-                    const int tok0 = (w.local + jj) * kPagedTile;
-                    ok = ok && wait(&s_ready[g], (uint32_t)sc & 1u);
-                    ++sc;
+                    const int jj = dual ? k : 2 * k + g;             // tile within the segment
+                    const int tile0 = (w.local + jj) * kPagedTile;   // its first token
+                    const int tok0 = tile0 + 64 * h;                 // this thread's
+                    ok = ok && wait(&s_ready[g], sph);
+                    sph ^= 1u;
                     tc_fence_after();
-                    if (ok && warp_live) {
-                        const bool mask = tok0 + kPagedTile - 1 > lim_lo;  // warp-uniform
-                        uint32_t pk[64];
-                        // P of the tile against reference r; returns its sum
+                    if (warp_live) {
+                        const bool mask = tok0 + 63 > lim_lo;  // warp-uniform
+                        uint32_t pk[32];
+                        // P of these tokens against reference r; returns their sum
                         auto exps = [&](float r) {
                             const float nref = r == -INFINITY ? 0.f : -r;
                             float s4[4] = {0.f, 0.f, 0.f, 0.f};
-                            uint32_t v[2][32];
-                            tmem_ld32_async(scol, v[0]);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                tmem_ld32_wait(v[c & 1]);
-                                if (c < 3) tmem_ld32_async(scol + 32u * (c + 1), v[(c + 1) & 1]);
-                                uint32_t (&x)[32] = v[c & 1];
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t x[32];
+                                tmem_ld32_async(scol + 32u * c, x);
+                                tmem_ld32_wait(x);
                                 if (neg) {
 #pragma unroll
                                     for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.scale_log2);
@@ -383,61 +471,73 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                             return (s4[0] + s4[1]) + (s4[2] + s4[3]);
                         };
                         float cs = 0.f;
-                        bool redo = ref == -INFINITY && lim >= tok0;  // the row's first keys
-                        const bool fresh = __all_sync(0xffffffffu, ref == -INFINITY);
-                        if (!fresh) {
+                        bool redo = ref == -INFINITY && lim >= tile0;  // the row's first keys
+                        const bool fresh = __all_sync(0xffffffffu, ref == -INFINITY);  // of both warps: they share ref
+                        if (ok && !fresh) {
                             cs = exps(ref);
                             redo = redo || cs > kSumLimit;
                         }
-                        if (fresh || __any_sync(0xffffffffu, redo)) {
+                        if (pair_any(pair_bar, redo)) {
+                            // the row's maximum over both halves becomes the reference
                             float r4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            if (ok) {
 #pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t x[32];
-                                tmem_ld32(scol + 32u * c, x);
+                                for (int c = 0; c < 2; ++c) {
+                                    uint32_t x[32];
+                                    tmem_ld32(scol + 32u * c, x);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    float y = __uint_as_float(x[e]);
-                                    if (neg) y *= p.scale_log2;
-                                    if (tok0 + 32 * c + e > lim) y = -INFINITY;
-                                    r4[e & 3] = fmaxf(r4[e & 3], y);
+                                    for (int e = 0; e < 32; ++e) {
+                                        float y = __uint_as_float(x[e]);
+                                        if (neg) y *= p.scale_log2;
+                                        if (tok0 + 32 * c + e > lim) y = -INFINITY;
+                                        r4[e & 3] = fmaxf(r4[e & 3], y);
+                                    }
                                 }
                             }
-                            const float top = fmaxf(fmaxf(r4[0], r4[1]), fmaxf(r4[2], r4[3])) * mul - kRefDrop;
+                            float top = fmaxf(fmaxf(r4[0], r4[1]), fmaxf(r4[2], r4[3])) * mul;
+                            float *slot = xchg + 128 * g + row;
+                            if (h == 1) *slot = top;
+                            named_bar_sync(pair_bar, 64);
+                            if (h == 0) *slot = top = fmaxf(top, *slot);
+                            named_bar_sync(pair_bar, 64);
+                            if (h == 1) top = *slot;
                             float alpha = 1.f;
-                            if (redo && top > ref) {
-                                alpha = fast_exp2(ref - top);  // 0 from no reference
-                                ref = top;
+                            if (top > ref + kRefMove) {  // any maximum, where there is no reference yet
+                                alpha = fast_exp2(ref - (top - kRefDrop));
+                                ref = top - kRefDrop;
                                 l *= alpha;
                             }
-                            if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                            if (ok && k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                                 // S of this tile is complete, hence every earlier PV of the group
 #pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
+                                for (int c = 0; c < D / 2; c += 32) {
                                     uint32_t o[32];
-                                    tmem_ld32(ocol + 32u * c, o);
+                                    tmem_ld32(ocol + (uint32_t)c, o);
 #pragma unroll
                                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tmem_st32(ocol + 32u * c, o);
+                                    tmem_st32(ocol + (uint32_t)c, o);
                                 }
                             }
-                            cs = exps(ref);
+                            if (ok) cs = exps(ref);
+                        } else if (fresh) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) pk[e] = 0u;  // every row of the pair is masked in this tile
                         }
                         l += cs;
-                        tmem_st32(scol, *reinterpret_cast<uint32_t (*)[32]>(&pk[0]));
-                        tmem_st32(scol + 32u, *reinterpret_cast<uint32_t (*)[32]>(&pk[32]));
-                        tmem_wait_st();
+                        if (ok) {
+                            tmem_st32(scol, pk);  // over the first half of the scores it read
+                            tmem_wait_st();
+                        }
                     }
                     // rows of the last page past the request may hold anything: zero
                     // them, so that 0 * NaN cannot reach O (pages past it read zeros)
-                    if (ok && (g == 0 || !dual) && w.s.len < tok0 + kPagedTile && (w.s.len & (p.S - 1)) != 0) {
-                        const int v = vc + jj, s = v % C::NV;
-                        ok = wait(&vfull[s], (uint32_t)(v / C::NV) & 1u);
-                        if (ok && tok0 + row >= w.s.len) {
+                    if (ok && (g == 0 || !dual) && w.s.len < tile0 + kPagedTile && (w.s.len & (p.S - 1)) != 0) {
+                        const int s = (vs + jj) % C::NV;
+                        ok = wait(&vfull[s], vp ^ ((uint32_t)((vs + jj) / C::NV) & 1u));
+                        if (ok && tile0 + row >= w.s.len && h < C::KH) {
 #pragma unroll
-                            for (int q = 0; q < 8 * C::KH; ++q)
-                                *reinterpret_cast<uint4 *>(sv + s * C::TILE + (q >> 3) * C::BLK + row * 128 + (q & 7) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4 *>(sv + s * C::TILE + h * C::BLK + row * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
@@ -445,46 +545,54 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&p_ready[g]));
                 }
-                vc += n;
+                vp ^= (uint32_t)((vs + n) / C::NV) & 1u;
+                vs = (vs + n) % C::NV;
 
-                // ---- epilogue ----
+                // ---- epilogue: sums of the two halves, then of the two groups if they share the rows ----
                 if (nx > 0) {
-                    ok = ok && wait(&o_done[g], (uint32_t)oc & 1u);
-                    ++oc;
+                    ok = ok && wait(&o_done[g], oph);
+                    oph ^= 1u;
                 }
-                tc_fence_after();
+                tc_fence_before();
                 const bool whole = w.whole();
                 float w0 = 1.f, w1 = 0.f;  // weights of O0 and O1 (one row tile), or w0 of this group's O
                 float M = ref, L = l;
+                if (h == 1) xchg[128 * g + row] = l;
+                named_bar_sync(1, 512);
+                if (h == 0) L = l + xchg[128 * g + row];
+                float2 *both = reinterpret_cast<float2 *>(xchg);
                 if (!dual) {
-                    if (g == 1) xchg[row] = make_float2(ref, l);
-                    tc_fence_before();
-                    named_bar_sync(1, 256);
-                    if (g == 0) {
-                        const float2 o = xchg[row];
+                    named_bar_sync(1, 512);
+                    if (g == 1 && h == 0) both[row] = make_float2(ref, L);
+                    named_bar_sync(1, 512);
+                    if (g == 0 && h == 0) {
+                        const float2 o = both[row];
                         M = fmaxf(ref, o.x);
                         w0 = ref == -INFINITY ? 0.f : fast_exp2(ref - M);
                         w1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - M);
-                        L = w0 * l + w1 * o.y;
+                        L = w0 * L + w1 * o.y;
                         if (whole) {
                             const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
                             w0 *= inv;
                             w1 *= inv;
                         }
-                        xchg[row] = make_float2(w0, w1);
+                        both[row] = make_float2(w0, w1);
                     }
-                    named_bar_sync(1, 256);
-                    tc_fence_after();
-                    if (g == 1) {
-                        const float2 o = xchg[row];
-                        w0 = o.x;
-                        w1 = o.y;
+                    named_bar_sync(1, 512);
+                    const float2 o = both[row];
+                    w0 = o.x;
+                    w1 = o.y;
+                } else {
+                    if (h == 0) {
+                        if (whole) w0 = L > 0.f || L != L ? 1.f / L : 0.f;
+                        xchg[128 * g + row] = w0;
                     }
-                } else if (whole) {
-                    w0 = L > 0.f || L != L ? 1.f / L : 0.f;
+                    named_bar_sync(1, 512);
+                    w0 = xchg[128 * g + row];
                 }
-                // this thread's share: its row's D channels (two row tiles), or half of them
-                const int c0 = dual ? 0 : g * (D / 2), nc = dual ? D : D / 2;
+                tc_fence_after();
+                // this thread's share of its row's D channels: half of them, or a quarter where four threads share it
+                const int nc = dual ? D / 2 : D / 4, c0 = dual ? h * nc : (2 * g + h) * nc;
                 const uint32_t o0 = tlane + C::O_COL + (dual ? 128u * (uint32_t)g : 0u), o1 = tlane + C::O_COL + 128u;
                 const bool second = !dual && n > 1;
                 const int q_row = w.s.q0 + w.rb * TB + (rho >> p.gshift);
@@ -492,45 +600,38 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const int slot = w.first ? 0 : 1;
                 float *part = p.part + ((int64_t)blockIdx.x * 2 + slot) * C::PART;
                 if (warp_live) {
-                    if (!whole && live && (dual || g == 0)) reinterpret_cast<float2 *>(part)[rho] = make_float2(M, L);
+                    if (!whole && live && h == 0 && (dual || g == 0)) reinterpret_cast<float2 *>(part)[rho] = make_float2(M, L);
 #pragma unroll 1
-                    for (int c = c0; c < c0 + nc; c += 32) {
-                        uint32_t a[32];
-                        if (ok) {
-                            tmem_ld32(o0 + (uint32_t)c, a);
-                        } else {
+                    for (int c = c0; c < c0 + nc; c += 16) {
+                        uint32_t a[16], b[16];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) a[e] = 0u;
+                        for (int e = 0; e < 16; ++e) a[e] = b[e] = 0u;
+                        if (ok) {
+                            tmem_ld16(o0 + (uint32_t)c, a);
+                            if (second) tmem_ld16(o1 + (uint32_t)c, b);
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) a[e] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(a[e]) * w0);
-                        if (second) {
-                            uint32_t b[32];
-                            if (ok) {
-                                tmem_ld32(o1 + (uint32_t)c, b);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) b[e] = 0u;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (w1 != 0.f) a[e] = __float_as_uint(fmaf(__uint_as_float(b[e]), w1, __uint_as_float(a[e])));
+                        for (int e = 0; e < 16; ++e) {
+                            // a weight of zero: no keys, and nothing of that O may count
+                            float y = w0 == 0.f ? 0.f : __uint_as_float(a[e]) * w0;
+                            if (second && w1 != 0.f) y = fmaf(__uint_as_float(b[e]), w1, y);
+                            a[e] = __float_as_uint(y);
                         }
                         if (!live) continue;
                         if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint4 h;
-                                h.x = pack2<BF16>(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-                                h.y = pack2<BF16>(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
-                                h.z = pack2<BF16>(__uint_as_float(a[e + 4]), __uint_as_float(a[e + 5]));
-                                h.w = pack2<BF16>(__uint_as_float(a[e + 6]), __uint_as_float(a[e + 7]));
-                                *reinterpret_cast<uint4 *>(dst + c + e) = h;
+                            for (int e = 0; e < 16; e += 8) {
+                                uint4 x;
+                                x.x = pack2<BF16>(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+                                x.y = pack2<BF16>(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
+                                x.z = pack2<BF16>(__uint_as_float(a[e + 4]), __uint_as_float(a[e + 5]));
+                                x.w = pack2<BF16>(__uint_as_float(a[e + 6]), __uint_as_float(a[e + 7]));
+                                *reinterpret_cast<uint4 *>(dst + c + e) = x;
                             }
                         } else {
                             float4 *acc = reinterpret_cast<float4 *>(part + C::ML) + (int64_t)(c / 4) * C::RB + rho;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
+                            for (int e = 0; e < 16; e += 4)
                                 acc[(e / 4) * C::RB] = make_float4(__uint_as_float(a[e]), __uint_as_float(a[e + 1]),
                                                                    __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
                         }
@@ -539,6 +640,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(o_free));
+                named_bar_sync(1, 512);  // xchg is free again; partial stores are done
 
                 if (!whole) {
                     // ---- arrive at the split item; the last arrival merges it ----
@@ -546,7 +648,6 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     const int gp = sched->grid;
                     const int64_t c_lo = tile_owner(w.off, T, gp);
                     const int np = (int)(tile_owner(w.off + w.tiles - 1, T, gp) - c_lo) + 1;
-                    named_bar_sync(1, 256);
                     if (tid == 0) {
                         // the barrier orders every thread's partial stores before this
                         // release; the last arrival acquires all of them
@@ -555,7 +656,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         if (last) p.count[c_lo] = 0u;
                         sched->last = last;
                     }
-                    named_bar_sync(1, 256);
+                    named_bar_sync(1, 512);
                     if (sched->last && live) {
                         // partials: slot 0 (a range's first segment), but the first CTA's,
                         // which is its last unless the item begins its range
@@ -570,10 +671,10 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         }
                         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll 1
-                        for (int c = c0; c < c0 + nc; c += 32) {
-                            float4 a[8];
+                        for (int c = c0; c < c0 + nc; c += 16) {
+                            float4 a[4];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                             for (int i = 0; i < np; ++i) {
                                 const float *pi = part_of(i);
@@ -581,7 +682,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                 const float f = m == -INFINITY ? 0.f : fast_exp2(m - mx) * inv;
                                 const float4 *acc = reinterpret_cast<const float4 *>(pi + C::ML) + (int64_t)(c / 4) * C::RB + rho;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
+                                for (int e = 0; e < 4; ++e) {
                                     const float4 x = __ldcg(acc + e * C::RB);
                                     a[e].x = fmaf(f, x.x, a[e].x);
                                     a[e].y = fmaf(f, x.y, a[e].y);
@@ -590,13 +691,13 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                 }
                             }
 #pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                uint4 h;
-                                h.x = pack2<BF16>(a[e].x, a[e].y);
-                                h.y = pack2<BF16>(a[e].z, a[e].w);
-                                h.z = pack2<BF16>(a[e + 1].x, a[e + 1].y);
-                                h.w = pack2<BF16>(a[e + 1].z, a[e + 1].w);
-                                *reinterpret_cast<uint4 *>(dst + c + 4 * e) = h;
+                            for (int e = 0; e < 4; e += 2) {
+                                uint4 x;
+                                x.x = pack2<BF16>(a[e].x, a[e].y);
+                                x.y = pack2<BF16>(a[e].z, a[e].w);
+                                x.z = pack2<BF16>(a[e + 1].x, a[e + 1].y);
+                                x.w = pack2<BF16>(a[e + 1].z, a[e + 1].w);
+                                *reinterpret_cast<uint4 *>(dst + c + 4 * e) = x;
                             }
                         }
                     }
@@ -607,7 +708,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(512));
+    if (warp == 17) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(512));
 }
 
 template <int D, bool BF16>
