@@ -102,6 +102,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+// Two 32-bit floats in a register pair, and their packed arithmetic (each
+// element rounded as by the scalar instruction, in half the issue slots).
+__device__ __forceinline__ uint64_t pair32(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair32(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // True on the 64 threads of barrier `id` when any of them passed true.
 __device__ __forceinline__ bool pair_any(int id, bool pred) {
     uint32_t r;
@@ -247,8 +270,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const int rows = min(TB, w.s.m - w.rb * TB) * p.G;
                 if (is_k) {
                     if (seg > 0) {
-                        if (lane == 0) ok = mbar_wait(smem_u32(qempty), (uint32_t)(seg - 1) & 1u, p.timeout_ns, abort_flag);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        ok = warp_mbar_wait(smem_u32(qempty), (uint32_t)(seg - 1) & 1u, p.timeout_ns, abort_flag);
                         if (!ok) break;
                     }
                     if (lane == 0) {
@@ -276,8 +298,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 for (int t = 0; t < n; ++t, ++i) {
                     const int s = i % NS;
                     if (i >= NS) {
-                        if (lane == 0) ok = mbar_wait(smem_u32(&empty[s]), ((uint32_t)(i / NS) & 1u) ^ 1u, p.timeout_ns, abort_flag);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        ok = warp_mbar_wait(smem_u32(&empty[s]), ((uint32_t)(i / NS) & 1u) ^ 1u, p.timeout_ns, abort_flag);
                         if (!ok) break;
                     }
                     const uint32_t fb = smem_u32(&full[s]);
@@ -322,8 +343,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             uint32_t sp = 0;                // phase of the segment's barriers
             bool first_seg = true, ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
-                return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.timeout_ns, abort_flag)) != 0;
+                return warp_mbar_wait(smem_u32(bar), parity, p.timeout_ns, abort_flag);
             };
             auto segment = [&](auto dual_c, int ne) {
                 constexpr bool DUAL = decltype(dual_c)::value;
@@ -411,9 +431,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             uint32_t vp = 0;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                bool r = true;
-                if (lane == 0) r = mbar_wait(smem_u32(bar), parity, p.timeout_ns, abort_flag);
-                r = __shfl_sync(0xffffffffu, r, 0);
+                const bool r = warp_mbar_wait(smem_u32(bar), parity, p.timeout_ns, abort_flag);
                 if (!r && lane == 0) {
                     raise_flag(p.status, GQAQ_DEV_TIMEOUT);
                     *abort_flag = 1;
@@ -445,7 +463,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         // P of these tokens against reference r; returns their sum
                         auto exps = [&](float r) {
                             const float nref = r == -INFINITY ? 0.f : -r;
-                            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                            const uint64_t mul2 = pair32(mul, mul), nref2 = pair32(nref, nref);
+                            uint64_t sum0 = 0, sum1 = 0;  // two pairs of partial sums
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 uint32_t x[32];
@@ -462,13 +481,15 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                 }
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    const float e0 = fast_exp2(fmaf(__uint_as_float(x[e]), mul, nref));
-                                    const float e1 = fast_exp2(fmaf(__uint_as_float(x[e + 1]), mul, nref));
-                                    s4[(e >> 1) & 3] += e0 + e1;
+                                    const float2 y = unpair32(fma2(pair32(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2, nref2));
+                                    const float e0 = fast_exp2(y.x), e1 = fast_exp2(y.y);
+                                    uint64_t &sum = (e & 2) ? sum1 : sum0;
+                                    sum = add2(sum, pair32(e0, e1));
                                     pk[16 * c + (e >> 1)] = pack2<BF16>(e0, e1);
                                 }
                             }
-                            return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                            const float2 t = unpair32(add2(sum0, sum1));
+                            return t.x + t.y;
                         };
                         float cs = 0.f;
                         bool redo = ref == -INFINITY && lim >= tile0;  // the row's first keys

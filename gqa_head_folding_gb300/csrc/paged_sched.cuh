@@ -100,6 +100,22 @@ __device__ __forceinline__ int64_t head_tiles(const PagedSeq &s, int tbs) {
     return tiles_before(s, last, tbs) + block_tiles(s, last, tbs);
 }
 
+// Bounded wait of a converged warp for the phase with parity `parity`; false
+// on every lane when timeout_ns passed or *abort became nonzero first. The
+// clock and the flag are looked at once in 32 probes: a waiting warp shares
+// its scheduler with warps that compute.
+__device__ __forceinline__ bool warp_mbar_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int *abort) {
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *abort != 0 || now - t0 >= timeout_ns)) return false;
+    }
+}
+
 // What a CTA knows of its range.
 struct PagedSched {
     int64_t T, t_begin, t_end;  // tiles of all items; this CTA's range
