@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             const uint32_t tlane = tbase + ((uint32_t)((warp & 3) * 32) << 16);
             const uint32_t scol = tlane + C::S_COL + 128u * (uint32_t)g + 64u * (uint32_t)h;
             const uint32_t ocol = tlane + C::O_COL + 128u * (uint32_t)g + (uint32_t)(h * (D / 2));  // the half it rescales
-            const bool neg = !(p.scale_log2 > 0.f);  // a positive scale folds into the exponent
-            const float mul = neg ? 1.f : p.scale_log2;
+            const float mul = p.scale_log2;              // any sign, not zero
+            const float hide = mul > 0.f ? -INFINITY : INFINITY;  // a masked score: its product is -inf
             uint32_t sph = 0, oph = 0;  // phases of s_ready and o_done
             int vs = 0;                 // V slot of the segment's first tile, and its phase
             uint32_t vp = 0;
@@ -470,14 +470,10 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                 uint32_t x[32];
                                 tmem_ld32_async(scol + 32u * c, x);
                                 tmem_ld32_wait(x);
-                                if (neg) {
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.scale_log2);
-                                }
-                                if (mask) {
+                                if (__builtin_expect(mask, 0)) {
 #pragma unroll
                                     for (int e = 0; e < 32; ++e)
-                                        if (tok0 + 32 * c + e > lim) x[e] = __float_as_uint(-INFINITY);
+                                        if (tok0 + 32 * c + e > lim) x[e] = __float_as_uint(hide);
                                 }
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
@@ -492,13 +488,21 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                             return t.x + t.y;
                         };
                         float cs = 0.f;
-                        bool redo = ref == -INFINITY && lim >= tile0;  // the row's first keys
                         const bool fresh = __all_sync(0xffffffffu, ref == -INFINITY);  // of both warps: they share ref
-                        if (ok && !fresh) {
-                            cs = exps(ref);
-                            redo = redo || cs > kSumLimit;
-                        }
-                        if (pair_any(pair_bar, redo)) {
+                        // one copy of the exponentials serves both passes: the second, after a
+                        // row's reference has moved, is rare, and code that is jumped over costs fetches
+#pragma unroll 1
+                        for (int pass = fresh ? 0 : 1;; ++pass) {
+                            if (pass > 0 && ok) cs = exps(ref);
+                            if (pass > 1) break;
+                            const bool redo = (ref == -INFINITY && lim >= tile0) || cs > kSumLimit;  // the row's first keys, or far above
+                            if (__builtin_expect(!pair_any(pair_bar, redo), 1)) {
+                                if (pass == 0) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) pk[e] = 0u;  // every row of the pair is masked in this tile
+                                }
+                                break;
+                            }
                             // the row's maximum over both halves becomes the reference
                             float r4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                             if (ok) {
@@ -508,14 +512,12 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                     tmem_ld32(scol + 32u * c, x);
 #pragma unroll
                                     for (int e = 0; e < 32; ++e) {
-                                        float y = __uint_as_float(x[e]);
-                                        if (neg) y *= p.scale_log2;
-                                        if (tok0 + 32 * c + e > lim) y = -INFINITY;
+                                        const float y = tok0 + 32 * c + e > lim ? -INFINITY : __uint_as_float(x[e]) * mul;
                                         r4[e & 3] = fmaxf(r4[e & 3], y);
                                     }
                                 }
                             }
-                            float top = fmaxf(fmaxf(r4[0], r4[1]), fmaxf(r4[2], r4[3])) * mul;
+                            float top = fmaxf(fmaxf(r4[0], r4[1]), fmaxf(r4[2], r4[3]));
                             float *slot = xchg + 128 * g + row;
                             if (h == 1) *slot = top;
                             named_bar_sync(pair_bar, 64);
@@ -539,10 +541,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                     tmem_st32(ocol + (uint32_t)c, o);
                                 }
                             }
-                            if (ok) cs = exps(ref);
-                        } else if (fresh) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) pk[e] = 0u;  // every row of the pair is masked in this tile
+                            pass = 1;  // the next pass is the last
                         }
                         l += cs;
                         if (ok) {
@@ -762,6 +761,7 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     p.S = d.page_size;
     p.zero_row = (int)rows;
     p.scale_log2 = a.scale * 1.4426950408889634f;
+    if (p.scale_log2 == 0.f) p.scale_log2 = 1e-30f;  // 2^(s - max) is 1 all the same, and a masked score's product stays -inf
     p.timeout_ns = ctx.timeout_ns;
     p.test_stall = ctx.test_stall;
     const cudaError_t e = launch_kernel(paged_tc_kernel<D, BF16>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, ctx, 0, qmap,

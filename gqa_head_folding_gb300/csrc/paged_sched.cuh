@@ -100,19 +100,34 @@ __device__ __forceinline__ int64_t head_tiles(const PagedSeq &s, int tbs) {
     return tiles_before(s, last, tbs) + block_tiles(s, last, tbs);
 }
 
+// Up to 64 probes of a barrier's phase in the shortest loop there is: a
+// waiting warp shares its scheduler with warps that compute (with a vote, a
+// clock and a sleep between probes, waiting took half of all issue slots).
+__device__ __forceinline__ bool mbar_probe64(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, c;\n\t.reg .u32 n;\n\tmov.u32 n, 16;\n"
+        "AGAIN_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE_%=;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE_%=;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE_%=;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE_%=;\n\t"
+        "sub.u32 n, n, 1;\n\tsetp.ne.u32 c, n, 0;\n\t@c bra AGAIN_%=;\n"
+        "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait of a converged warp for the phase with parity `parity`; false
-// on every lane when timeout_ns passed or *abort became nonzero first. The
-// clock and the flag are looked at once in 32 probes: a waiting warp shares
-// its scheduler with warps that compute.
+// on every lane when timeout_ns passed or *abort became nonzero first.
 __device__ __forceinline__ bool warp_mbar_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int *abort) {
-    uint64_t t0 = 0;
+    if (__all_sync(0xffffffffu, mbar_probe64(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
     while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (__any_sync(0xffffffffu, *abort != 0 || now - t0 >= timeout_ns)) return false;
+        if (__all_sync(0xffffffffu, mbar_probe64(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - t0 >= timeout_ns)) return false;
     }
 }
 
