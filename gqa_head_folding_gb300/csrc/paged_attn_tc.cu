@@ -183,6 +183,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
+// The softmax warps' place in the CTA's range. One thread moves it on and all
+// read it from shared memory: held by each thread it spilled registers of the
+// loop over tiles, whose reloads missed the small L1 that is left beside the
+// tiles (2 of 3.5 thousand cycles per tile).
+struct PtcSegment {
+    PagedWalk w;
+    int v_before;  // V tiles before this segment
+    int more;
+};
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -208,8 +218,9 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     uint64_t *drain = o_free + 1;
     int64_t *scratch = reinterpret_cast<int64_t *>(drain + 1);  // [8]
     PagedSched *sched = reinterpret_cast<PagedSched *>(scratch + 8);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sched + 1);
-    static_assert(256 * 4 + (2 * C::NK + 2 * C::NV + 10 + 8) * 8 + sizeof(PagedSched) + 8 <= C::MISC, "misc region");
+    PtcSegment *seg_s = reinterpret_cast<PtcSegment *>(sched + 1);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(seg_s + 1);
+    static_assert(256 * 4 + (2 * C::NK + 2 * C::NV + 10 + 8) * 8 + sizeof(PagedSched) + sizeof(PtcSegment) + 8 <= C::MISC, "misc region");
     volatile int *abort_flag = &sched->abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -250,12 +261,12 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
 
     if (work) {
         const int TB = C::RB >> p.gshift;  // tokens of an item
-        PagedWalk w;
-        w.init(p.w, *sched);
         if ((warp == 16 || warp == 18) && !p.test_stall) {
             // --------------------------------------------------------------
             // Loaders: K (and Q) in warp 16, V in warp 18. A lane per page.
             // --------------------------------------------------------------
+            PagedWalk w;
+            w.init(p.w, *sched);
             const bool is_k = warp == 16;
             const int NS = is_k ? C::NK : C::NV;
             uint64_t *full = is_k ? kfull : vfull, *empty = is_k ? kempty : vempty;
@@ -332,6 +343,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             // S(e + 2) follows PV(e), which frees its tensor memory: the core
             // runs one thread's MMAs in order.
             // --------------------------------------------------------------
+            PagedWalk w;
+            w.init(p.w, *sched);
             constexpr uint32_t IDESC_S = umma_idesc(128, 128, 0, BF16);
             constexpr uint32_t IDESC_O = umma_idesc(128, D, 1, BF16);
             const uint64_t qdesc0 = umma_desc(smem_u32(sq), 16);
@@ -427,9 +440,13 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             const float mul = p.scale_log2;              // any sign, not zero
             const float hide = mul > 0.f ? -INFINITY : INFINITY;  // a masked score: its product is -inf
             uint32_t sph = 0, oph = 0;  // phases of s_ready and o_done
-            int vs = 0;                 // V slot of the segment's first tile, and its phase
-            uint32_t vp = 0;
             bool ok = true;
+            if (tid == 0) {
+                seg_s->w.init(p.w, *sched);
+                seg_s->v_before = 0;
+            }
+            named_bar_sync(1, 512);
+            const PagedWalk &w = seg_s->w;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 const bool r = warp_mbar_wait(smem_u32(bar), parity, p.timeout_ns, abort_flag);
                 if (!r && lane == 0) {
@@ -447,12 +464,13 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const int rho = r0 + row;                           // this thread's
                 const bool live = rho < rows, warp_live = r0 + (warp & 3) * 32 < rows;
                 const int pos0 = w.s.start + w.rb * TB;             // the block's first position
+                const int first0 = w.local * kPagedTile, len = w.s.len;
                 const int lim = pos0 + (rho >> p.gshift);           // this row's
                 const int lim_lo = pos0 + ((r0 + (warp & 3) * 32) >> p.gshift);  // the warp's least
                 float ref = -INFINITY, l = 0.f;
                 for (int k = 0; k < nx; ++k) {
                     const int jj = dual ? k : 2 * k + g;             // tile within the segment
-                    const int tile0 = (w.local + jj) * kPagedTile;   // its first token
+                    const int tile0 = first0 + jj * kPagedTile;      // its first token
                     const int tok0 = tile0 + 64 * h;                 // this thread's
                     ok = ok && wait(&s_ready[g], sph);
                     sph ^= 1u;
@@ -551,10 +569,10 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     }
                     // rows of the last page past the request may hold anything: zero
                     // them, so that 0 * NaN cannot reach O (pages past it read zeros)
-                    if (ok && (g == 0 || !dual) && w.s.len < tile0 + kPagedTile && (w.s.len & (p.S - 1)) != 0) {
-                        const int s = (vs + jj) % C::NV;
-                        ok = wait(&vfull[s], vp ^ ((uint32_t)((vs + jj) / C::NV) & 1u));
-                        if (ok && tile0 + row >= w.s.len && h < C::KH) {
+                    if (__builtin_expect(ok && (g == 0 || !dual) && len < tile0 + kPagedTile && (len & (p.S - 1)) != 0, 0)) {
+                        const int v = seg_s->v_before + jj, s = v % C::NV;
+                        ok = wait(&vfull[s], (uint32_t)(v / C::NV) & 1u);
+                        if (ok && tile0 + row >= len && h < C::KH) {
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
                                 *reinterpret_cast<uint4 *>(sv + s * C::TILE + h * C::BLK + row * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -565,8 +583,6 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&p_ready[g]));
                 }
-                vp ^= (uint32_t)((vs + n) / C::NV) & 1u;
-                vs = (vs + n) % C::NV;
 
                 // ---- epilogue: sums of the two halves, then of the two groups if they share the rows ----
                 if (nx > 0) {
@@ -722,7 +738,13 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         }
                     }
                 }
-            } while (w.next(w.seg_len(), p.w));
+                named_bar_sync(1, 512);  // the segment has been read
+                if (tid == 0) {
+                    seg_s->v_before += n;
+                    seg_s->more = seg_s->w.next(n, p.w);
+                }
+                named_bar_sync(1, 512);
+            } while (seg_s->more);
         }
     }
 
