@@ -39,7 +39,7 @@ namespace {
 
 template <int D>
 struct PtcCfg {
-    static constexpr int THREADS = 608;              // 16 softmax warps, K, MMA, V
+    static constexpr int THREADS = 640;              // 16 softmax warps, K, MMA, V, notifier
     static constexpr int RB = 256;                   // rows per item
     static constexpr int KH = D / 64;                // 64-channel blocks
     static constexpr int BLK = 128 * 128;            // one block of 128 rows
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const int rows = min(TB, w.s.m - w.rb * TB) * p.G;
                 if (is_k) {
                     if (seg > 0) {
-                        ok = warp_mbar_wait(smem_u32(qempty), (uint32_t)(seg - 1) & 1u, p.timeout_ns, abort_flag);
+                        ok = warp_mbar_wait_slow(smem_u32(qempty), (uint32_t)(seg - 1) & 1u, p.timeout_ns, abort_flag);
                         if (!ok) break;
                     }
                     if (lane == 0) {
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 for (int t = 0; t < n; ++t, ++i) {
                     const int s = i % NS;
                     if (i >= NS) {
-                        ok = warp_mbar_wait(smem_u32(&empty[s]), ((uint32_t)(i / NS) & 1u) ^ 1u, p.timeout_ns, abort_flag);
+                        ok = warp_mbar_wait_slow(smem_u32(&empty[s]), ((uint32_t)(i / NS) & 1u) ^ 1u, p.timeout_ns, abort_flag);
                         if (!ok) break;
                     }
                     const uint32_t fb = smem_u32(&full[s]);
@@ -426,6 +426,35 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             warp_commit(smem_u32(drain));  // every issued MMA completes before TMEM is released
             mbar_wait(smem_u32(drain), 0u, p.timeout_ns, nullptr);
             __syncwarp();
+        } else if (warp == 19) {
+            // --------------------------------------------------------------
+            // Notifier: watches the S barriers for the softmax warps, which wait
+            // at a hardware barrier per group instead. Sixteen warps that probe
+            // a shared-memory barrier fill the queue that every arrival and
+            // every other barrier goes through.
+            // --------------------------------------------------------------
+            PagedWalk w;
+            w.init(p.w, *sched);
+            uint32_t sph = 0;
+            bool ok = true;
+            do {
+                const int n = w.seg_len();
+                const int ne = min(TB, w.s.m - w.rb * TB) * p.G > 128 ? 2 * n : n;
+                for (int e = 0; e < ne; ++e) {
+                    const int x = e & 1;
+                    if (ok) {
+                        ok = warp_mbar_wait(smem_u32(&s_ready[x]), (sph >> x) & 1u, p.timeout_ns, abort_flag);
+                        if (!ok && lane == 0) {
+                            raise_flag(p.status, GQAQ_DEV_TIMEOUT);
+                            *abort_flag = 1;
+                        }
+                    }
+                    sph ^= 1u << x;
+                    tc_fence_after();
+                    tc_fence_before();
+                    named_bar_sync(10 + x, 288);  // also after a timeout: the groups pass once per tile
+                }
+            } while (w.next(w.seg_len(), p.w));
         } else if (warp < 16) {
             // --------------------------------------------------------------
             // Softmax groups: two threads per row, tokens 64 h .. 64 h + 63 of
@@ -439,7 +468,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             const uint32_t ocol = tlane + C::O_COL + 128u * (uint32_t)g + (uint32_t)(h * (D / 2));  // the half it rescales
             const float mul = p.scale_log2;              // any sign, not zero
             const float hide = mul > 0.f ? -INFINITY : INFINITY;  // a masked score: its product is -inf
-            uint32_t sph = 0, oph = 0;  // phases of s_ready and o_done
+            uint32_t oph = 0;  // phase of o_done
             bool ok = true;
             if (tid == 0) {
                 seg_s->w.init(p.w, *sched);
@@ -472,8 +501,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     const int jj = dual ? k : 2 * k + g;             // tile within the segment
                     const int tile0 = first0 + jj * kPagedTile;      // its first token
                     const int tok0 = tile0 + 64 * h;                 // this thread's
-                    ok = ok && wait(&s_ready[g], sph);
-                    sph ^= 1u;
+                    named_bar_sync(10 + g, 288);  // S is complete (after a timeout it holds anything)
                     tc_fence_after();
                     if (warp_live) {
                         const bool mask = tok0 + 63 > lim_lo;  // warp-uniform
@@ -511,7 +539,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         // row's reference has moved, is rare, and code that is jumped over costs fetches
 #pragma unroll 1
                         for (int pass = fresh ? 0 : 1;; ++pass) {
-                            if (pass > 0 && ok) cs = exps(ref);
+                            if (pass > 0) cs = exps(ref);
                             if (pass > 1) break;
                             const bool redo = (ref == -INFINITY && lim >= tile0) || cs > kSumLimit;  // the row's first keys, or far above
                             if (__builtin_expect(!pair_any(pair_bar, redo), 1)) {
@@ -523,16 +551,14 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                             }
                             // the row's maximum over both halves becomes the reference
                             float r4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                            if (ok) {
 #pragma unroll 1
-                                for (int c = 0; c < 2; ++c) {
-                                    uint32_t x[32];
-                                    tmem_ld32(scol + 32u * c, x);
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t x[32];
+                                tmem_ld32(scol + 32u * c, x);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) {
-                                        const float y = tok0 + 32 * c + e > lim ? -INFINITY : __uint_as_float(x[e]) * mul;
-                                        r4[e & 3] = fmaxf(r4[e & 3], y);
-                                    }
+                                for (int e = 0; e < 32; ++e) {
+                                    const float y = tok0 + 32 * c + e > lim ? -INFINITY : __uint_as_float(x[e]) * mul;
+                                    r4[e & 3] = fmaxf(r4[e & 3], y);
                                 }
                             }
                             float top = fmaxf(fmaxf(r4[0], r4[1]), fmaxf(r4[2], r4[3]));
@@ -548,7 +574,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                                 ref = top - kRefDrop;
                                 l *= alpha;
                             }
-                            if (ok && k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                            if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                                 // S of this tile is complete, hence every earlier PV of the group
 #pragma unroll 1
                                 for (int c = 0; c < D / 2; c += 32) {
@@ -562,10 +588,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                             pass = 1;  // the next pass is the last
                         }
                         l += cs;
-                        if (ok) {
-                            tmem_st32(scol, pk);  // over the first half of the scores it read
-                            tmem_wait_st();
-                        }
+                        tmem_st32(scol, pk);  // over the first half of the scores it read
+                        tmem_wait_st();
                     }
                     // rows of the last page past the request may hold anything: zero
                     // them, so that 0 * NaN cannot reach O (pages past it read zeros)

@@ -131,6 +131,16 @@ __device__ __forceinline__ bool warp_mbar_wait(uint32_t bar, uint32_t parity, ui
     }
 }
 
+// The same with sleeps between probes, for warps whose waits are not urgent.
+__device__ __forceinline__ bool warp_mbar_wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int *abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - t0 >= timeout_ns)) return false;
+    }
+}
+
 // What a CTA knows of its range.
 struct PagedSched {
     int64_t T, t_begin, t_end;  // tiles of all items; this CTA's range
