@@ -10,11 +10,6 @@ namespace {
 
 constexpr int kTabThreads = 1024;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -60,10 +55,10 @@ struct TablesParams {
     int B, T, S, shift, num_pages, max_pages;
 };
 
-// One cluster. Every CTA repeats the two prefix sums over the requests (new
+// Every CTA repeats the two prefix sums over the requests (new
 // rows, needed pages) from the same inputs, so that nothing but the final
 // count has to be exchanged; the rows and the new table entries are then
-// shared out over the cluster's threads, each finding its request by a binary
+// shared out over the grid's threads, each finding its request by a binary
 // search of the sums in shared memory. A new page's index follows from the
 // sums and the free list alone, so no thread waits for another's table entry.
 __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesParams p) {
@@ -73,7 +68,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
     int *base = np + p.B + 1;    // [B] tokens in the cache; -1: refused
     __shared__ int64_t buf[32];
     __shared__ int granted;      // new pages handed out
-    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    const int tid = threadIdx.x, rank = (int)blockIdx.x;
     const int nthreads = (int)blockDim.x, nctas = (int)gridDim.x;
     if (tid == 0) granted = 0;
     pdl_wait_and_release();
@@ -152,7 +147,8 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
         p.table[(int64_t)b * p.max_pages + held + (j - np[b])] = page;
     }
     if (flags) raise_flag(p.status, flags);
-    cluster_sync_all();  // every CTA has read the count, which may be replaced in place
+    // a count replaced in place: one cluster, whose CTAs have all read it (else a cluster is one CTA)
+    cluster_sync_all();
     if (rank == 0 && tid == 0) *p.free_count_out = count - granted;
 }
 
@@ -163,14 +159,14 @@ struct ReleaseParams {
     int B, S, shift, num_pages, max_pages;
 };
 
-// One cluster, the same shape as the plan: every CTA sums the pages that
+// The same shape as the plan: every CTA sums the pages that
 // leave, then each thread moves some of them.
 __global__ void __launch_bounds__(kTabThreads) paged_release_kernel(const ReleaseParams p) {
     extern __shared__ int sm[];
     int *cum = sm;               // [B + 1] leaving pages before each request
     int *from = cum + p.B + 1;   // [B] first leaving page
     __shared__ int64_t buf[32];
-    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    const int tid = threadIdx.x, rank = (int)blockIdx.x;
     const int nthreads = (int)blockDim.x, nctas = (int)gridDim.x;
     pdl_wait_and_release();
     const int raw_count = *p.free_count;
@@ -218,27 +214,31 @@ int log2_of(int s) {
     return k;
 }
 
-// CTAs of the one cluster: one up to 4096 elements of work, else up to eight.
-int table_ctas(int64_t work) {
+// CTAs: one up to 2048 elements of work. A count replaced in place needs the
+// cluster's barrier before it is written, hence at most eight CTAs; otherwise
+// up to 64 (each repeats the sums, so more would add little).
+int table_ctas(int64_t work, bool in_place) {
     int c = 1;
-    while (c < 8 && (int64_t)c * 4 * kTabThreads < work) c *= 2;
+    while (c < (in_place ? 8 : 64) && (int64_t)c * 2 * kTabThreads < work) c *= 2;
     return c;
 }
 
 template <typename P>
-int launch_tables(void (*kern)(P), const P &p, int words, int64_t work, const LaunchCtx &ctx) {
+int launch_tables(void (*kern)(P), const P &p, int words, int64_t work, bool in_place, const LaunchCtx &ctx) {
     const size_t smem = (size_t)words * sizeof(int);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return GQAQ_ERR_CUDA;
-    const int ctas = table_ctas(work);
-    const cudaError_t e = launch_kernel(kern, dim3((unsigned)ctas), dim3(kTabThreads), smem, ctx, ctas, p);
+    const int ctas = table_ctas(work, in_place);
+    const cudaError_t e = launch_kernel(kern, dim3((unsigned)ctas), dim3(kTabThreads), smem, ctx, in_place ? ctas : 0, p);
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
 // Norm, rotation and append
 // ---------------------------------------------------------------------------
+constexpr int kAppendRows = 2;  // rows of a token per thread
+
 struct AppendPagedParams {
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;
@@ -280,115 +280,160 @@ __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
     return make_uint4(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]), pack2<BF16>(y[4], y[5]), pack2<BF16>(y[6], y[7]));
 }
 
-// One CTA per token. D/16 lanes share a head's row; a lane holds two blocks of
-// eight channels: (8j, rope/2 + 8j), so that with the halves style both
-// members of every pair sit in one lane, and two neighbouring blocks where
-// nothing turns. The token's angles are loaded once and serve all its heads.
+// D/16 lanes share a head's row; a lane holds two blocks of eight channels:
+// (8j, rope/2 + 8j), so that with the halves style both members of every pair
+// sit in one lane, and two neighbouring blocks where nothing turns. A thread
+// owns the same two rows (heads) of every token its CTA takes, so the norm
+// weights stay in registers, a token's angles serve both rows, and the next
+// token's rows are loaded while this one's are computed: the kernel moves each
+// byte once and is bound by HBM (see launch_append_t for the shape).
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendPagedParams p) {
     constexpr int LPR = D / 16;         // lanes per row
-    constexpr int RPC = 256 / LPR;      // rows per pass of the CTA
+    constexpr int NP = kAppendRows;     // rows per thread
     pdl_wait_and_release();
-    const int t = blockIdx.x;
-    const int slot = p.slots[t];
-    if (slot < 0) return;
-    const int page = slot >> p.shift;
-    if (page >= p.num_pages) {
-        if (threadIdx.x == 0) raise_flag(p.status, GQAQ_DEV_BAD_PAGE);
-        return;
-    }
+    const int rpp = (int)blockDim.x / LPR;  // rows per pass
     const int j = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
     const int R = p.rope;
     const bool turns = 16 * j < R;
     const int c0 = turns ? 8 * j : 16 * j, c1 = turns ? R / 2 + 8 * j : 16 * j + 8;
-    float cs[16], sn[16];
-    if (R > 0) {
-        const int pos = p.positions[t];
-        if (pos < 0 || pos >= p.max_position) {
-            if (threadIdx.x == 0) raise_flag(p.status, GQAQ_DEV_BAD_POS);
-            return;
-        }
-        if (turns) {
-            const float *row = p.cos_sin + (int64_t)pos * R;
-            // halves: pair i of both blocks is channel 8j + i; adjacent pairs:
-            // a block of eight channels holds pairs c/2 .. c/2 + 3
-            const int i0 = INTER ? c0 / 2 : 8 * j, i1 = INTER ? c1 / 2 : 8 * j + 4;
-            const float4 a = *reinterpret_cast<const float4 *>(row + i0), b = *reinterpret_cast<const float4 *>(row + i1);
-            const float4 c = *reinterpret_cast<const float4 *>(row + R / 2 + i0), d = *reinterpret_cast<const float4 *>(row + R / 2 + i1);
-            cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w; cs[4] = b.x; cs[5] = b.y; cs[6] = b.z; cs[7] = b.w;
-            sn[0] = c.x; sn[1] = c.y; sn[2] = c.z; sn[3] = c.w; sn[4] = d.x; sn[5] = d.y; sn[6] = d.z; sn[7] = d.w;
+    // halves: pair i of both blocks is channel 8j + i; adjacent pairs: a block
+    // of eight channels holds pairs c/2 .. c/2 + 3
+    const int i0 = INTER ? c0 / 2 : 8 * j, i1 = INTER ? c1 / 2 : 8 * j + 4;
+    const int H = p.Hq + 2 * p.Hkv;
+    int head[NP], kind[NP];             // head within its tensor; 0 q, 1 k, 2 v, 3 none
+    uint4 wa[NP], wb[NP];
+    bool norm[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const int h = ((int)blockIdx.y * NP + n) * rpp + r0;
+        kind[n] = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : h < H ? 2 : 3;
+        head[n] = kind[n] == 0 ? h : kind[n] == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
+        const uint16_t *w = kind[n] == 0 ? p.q_weight : kind[n] == 1 ? p.k_weight : nullptr;
+        norm[n] = w != nullptr;
+        wa[n] = wb[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (norm[n]) {
+            wa[n] = *reinterpret_cast<const uint4 *>(w + c0);
+            wb[n] = *reinterpret_cast<const uint4 *>(w + c1);
         }
     }
-    const int H = p.Hq + 2 * p.Hkv;
-    // whole passes, so that the shuffles below see all lanes of a row's group
-    for (int h0 = 0; h0 < H; h0 += RPC) {
-        const int h = h0 + r0;
-        const bool live = h < H;
-        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-        const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        const uint16_t *src = is_q ? p.q + t * p.q_stride + h * D : is_v ? p.v + t * p.v_stride + hk * D : p.k + t * p.k_stride + hk * D;
-        uint16_t *dst = is_q ? p.q_out + ((int64_t)t * p.Hq + h) * D
-                             : (is_v ? p.v_pages : p.k_pages) + (((int64_t)page * p.Hkv + hk) * p.S + (slot & (p.S - 1))) * D;
-        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-        if (live) {
-            x0 = *reinterpret_cast<const uint4 *>(src + c0);
-            x1 = *reinterpret_cast<const uint4 *>(src + c1);
+    // a token's place, or -1: padding, or refused
+    auto place = [&](int t, int &pos) {
+        const int slot = p.slots[t];
+        pos = R > 0 ? p.positions[t] : 0;
+        int flags = 0;
+        if (slot < 0) return -1;
+        if ((slot >> p.shift) >= p.num_pages) flags |= GQAQ_DEV_BAD_PAGE;
+        if (R > 0 && (pos < 0 || pos >= p.max_position)) flags |= GQAQ_DEV_BAD_POS;
+        if (flags == 0) return slot;
+        if (threadIdx.x == 0 && blockIdx.y == 0) raise_flag(p.status, flags);
+        return -1;
+    };
+    auto load = [&](int t, uint4 (&x0)[NP], uint4 (&x1)[NP]) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            if (kind[n] == 3) continue;
+            const uint16_t *src = (kind[n] == 0 ? p.q + t * p.q_stride : kind[n] == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + head[n] * D;
+            x0[n] = *reinterpret_cast<const uint4 *>(src + c0);
+            x1[n] = *reinterpret_cast<const uint4 *>(src + c1);
         }
-        float a[8], b[8];
-        unpack8<BF16>(x0, a);
-        unpack8<BF16>(x1, b);
-        float ss = 0.f;
+    };
+    uint4 x0[NP], x1[NP], y0[NP], y1[NP];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (!live) continue;
-        if (!is_v) {
-            const uint16_t *w = is_q ? p.q_weight : p.k_weight;
-            if (w != nullptr) {
-                const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-                float wa[8], wb[8];
-                unpack8<BF16>(*reinterpret_cast<const uint4 *>(w + c0), wa);
-                unpack8<BF16>(*reinterpret_cast<const uint4 *>(w + c1), wb);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    a[e] = a[e] * inv * wa[e];
-                    b[e] = b[e] * inv * wb[e];
-                }
-            }
+    for (int n = 0; n < NP; ++n) x0[n] = x1[n] = y0[n] = y1[n] = make_uint4(0u, 0u, 0u, 0u);
+    int pos = 0, next_pos = 0;
+    int slot = place(blockIdx.x, pos);
+    if (slot >= 0) load(blockIdx.x, x0, x1);
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const int tn = t + (int)gridDim.x;
+        int next = -1;
+        if (tn < p.T) {
+            next = place(tn, next_pos);
+            if (next >= 0) load(tn, y0, y1);
+        }
+        if (slot >= 0) {  // the same for the whole CTA
+            float cs[8], sn[8];
             if (turns) {
-                if (INTER) {
+                const float *row = p.cos_sin + (int64_t)pos * R;
+                const float4 a = *reinterpret_cast<const float4 *>(row + i0), b = *reinterpret_cast<const float4 *>(row + i1);
+                const float4 c = *reinterpret_cast<const float4 *>(row + R / 2 + i0), d = *reinterpret_cast<const float4 *>(row + R / 2 + i1);
+                cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w; cs[4] = b.x; cs[5] = b.y; cs[6] = b.z; cs[7] = b.w;
+                sn[0] = c.x; sn[1] = c.y; sn[2] = c.z; sn[3] = c.w; sn[4] = d.x; sn[5] = d.y; sn[6] = d.z; sn[7] = d.w;
+            }
+            const int page = slot >> p.shift, row_in = slot & (p.S - 1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float u = a[2 * e], v = a[2 * e + 1], y = b[2 * e], z = b[2 * e + 1];
-                        a[2 * e] = u * cs[e] - v * sn[e];
-                        a[2 * e + 1] = v * cs[e] + u * sn[e];
-                        b[2 * e] = y * cs[4 + e] - z * sn[4 + e];
-                        b[2 * e + 1] = z * cs[4 + e] + y * sn[4 + e];
-                    }
-                } else {
+            for (int n = 0; n < NP; ++n) {
+                float a[8], b[8];
+                unpack8<BF16>(x0[n], a);
+                unpack8<BF16>(x1[n], b);
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+#pragma unroll
+                for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (kind[n] == 3) continue;
+                if (norm[n]) {
+                    const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+                    float u[8], v[8];
+                    unpack8<BF16>(wa[n], u);
+                    unpack8<BF16>(wb[n], v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float u = a[e], v = b[e];
-                        a[e] = u * cs[e] - v * sn[e];
-                        b[e] = v * cs[e] + u * sn[e];
+                        a[e] = a[e] * inv * u[e];
+                        b[e] = b[e] * inv * v[e];
                     }
                 }
-            }
-            if (w != nullptr || turns) {
-                x0 = pack8<BF16>(a);
-                x1 = pack8<BF16>(b);
+                const bool turn = turns && kind[n] != 2;
+                if (turn) {
+                    if (INTER) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = a[2 * e], v = a[2 * e + 1], y = b[2 * e], z = b[2 * e + 1];
+                            a[2 * e] = u * cs[e] - v * sn[e];
+                            a[2 * e + 1] = v * cs[e] + u * sn[e];
+                            b[2 * e] = y * cs[4 + e] - z * sn[4 + e];
+                            b[2 * e + 1] = z * cs[4 + e] + y * sn[4 + e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float u = a[e], v = b[e];
+                            a[e] = u * cs[e] - v * sn[e];
+                            b[e] = v * cs[e] + u * sn[e];
+                        }
+                    }
+                }
+                uint16_t *dst = kind[n] == 0 ? p.q_out + ((int64_t)t * p.Hq + head[n]) * D
+                                             : (kind[n] == 1 ? p.k_pages : p.v_pages) + (((int64_t)page * p.Hkv + head[n]) * p.S + row_in) * D;
+                const bool same = !norm[n] && !turn;  // nothing computed: the bits as they are
+                *reinterpret_cast<uint4 *>(dst + c0) = same ? x0[n] : pack8<BF16>(a);
+                *reinterpret_cast<uint4 *>(dst + c1) = same ? x1[n] : pack8<BF16>(b);
             }
         }
-        *reinterpret_cast<uint4 *>(dst + c0) = x0;
-        *reinterpret_cast<uint4 *>(dst + c1) = x1;
+        slot = next;
+        pos = next_pos;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            x0[n] = y0[n];
+            x1[n] = y1[n];
+        }
     }
 }
 
 template <int D, bool BF16>
 int launch_append_t(const AppendPagedParams &p, bool inter, const LaunchCtx &ctx) {
     auto kern = inter ? paged_append_kernel<D, BF16, true> : paged_append_kernel<D, BF16, false>;
-    const cudaError_t e = launch_kernel(kern, dim3((unsigned)p.T), dim3(256), 0, ctx, 0, p);
+    const int H = p.Hq + 2 * p.Hkv, lanes = D / 16;
+    // threads for half a token's rows (two rows each), in whole warps; more
+    // heads than 256 threads hold take more CTAs per token
+    int threads = ((H + kAppendRows - 1) / kAppendRows * lanes + 31) / 32 * 32;
+    if (threads > 256) threads = 256;
+    const int rows = threads / lanes * kAppendRows, gy = (H + rows - 1) / rows;
+    int per_sm = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) return GQAQ_ERR_CUDA;
+    int gx = per_sm * ctx.num_sms / gy;
+    gx = gx < 1 ? 1 : gx < p.T ? gx : p.T;
+    const cudaError_t e = launch_kernel(kern, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)threads), 0, ctx, 0, p);
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;
 }
 
@@ -414,7 +459,7 @@ int launch_paged_tables(const PagedTablesArgs &a, const LaunchCtx &ctx) {
     p.shift = log2_of(d.page_size);
     p.num_pages = d.num_pages;
     p.max_pages = d.max_pages;
-    return launch_tables(paged_tables_kernel, p, 3 * d.batch + 2, (int64_t)d.max_tokens + d.batch, ctx);
+    return launch_tables(paged_tables_kernel, p, 3 * d.batch + 2, (int64_t)d.max_tokens + d.batch, a.free_count == a.free_count_out, ctx);
 }
 
 int launch_paged_release(const PagedReleaseArgs &a, const LaunchCtx &ctx) {
@@ -433,7 +478,8 @@ int launch_paged_release(const PagedReleaseArgs &a, const LaunchCtx &ctx) {
     p.num_pages = d.num_pages;
     p.max_pages = d.max_pages;
     const int64_t table = (int64_t)d.batch * d.max_pages;  // at most this many pages leave, and at most the pool
-    return launch_tables(paged_release_kernel, p, 2 * d.batch + 1, table < d.num_pages ? table : d.num_pages, ctx);
+    return launch_tables(paged_release_kernel, p, 2 * d.batch + 1, table < d.num_pages ? table : d.num_pages,
+                         a.free_count == a.free_count_out, ctx);
 }
 
 int launch_paged_append(const PagedAppendArgs &a, const LaunchCtx &ctx) {
