@@ -237,8 +237,6 @@ int launch_tables(void (*kern)(P), const P &p, int words, int64_t work, bool in_
 // ---------------------------------------------------------------------------
 // Norm, rotation and append
 // ---------------------------------------------------------------------------
-constexpr int kAppendRows = 2;  // rows of a token per thread
-
 struct AppendPagedParams {
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;
@@ -249,20 +247,21 @@ struct AppendPagedParams {
     uint16_t *q_out, *k_pages, *v_pages;
     int *status;
     int T, Hq, Hkv, S, shift, num_pages, rope, max_position;
+    int stages, stage_bytes;  // the ring of tokens
+    uint64_t timeout_ns;
 };
 
+// Eight channels as four register pairs of 32-bit floats.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 &x, float (&y)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &x, f32x2 (&y)[4]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (BF16) {
-            y[2 * i] = __uint_as_float(w[i] << 16);
-            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            y[i] = pair32(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
         } else {
             const float2 f = half2_bits_to_float2(w[i]);
-            y[2 * i] = f.x;
-            y[2 * i + 1] = f.y;
+            y[i] = pair32(f.x, f.y);
         }
     }
 }
@@ -276,164 +275,270 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
-    return make_uint4(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]), pack2<BF16>(y[4], y[5]), pack2<BF16>(y[6], y[7]));
+__device__ __forceinline__ uint4 pack8(const f32x2 (&y)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpair32(y[i]);
+        w[i] = pack2<BF16>(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Bytes of shared memory a CTA's ring of tokens may take (two CTAs per SM).
+constexpr int kAppendRing = 96 * 1024;
+constexpr int kAppendStages = 6;        // tokens in flight at most
+constexpr int kAppendThreads = 256;     // consumer threads
+
+// What the loader leaves beside a token's rows.
+struct alignas(16) AppendToken {
+    int slot;  // -1: padding, or refused
+    int pad[3];
+};
+
+// Persistent CTAs over tokens; blockIdx.y takes a range of the token's rows
+// (q heads, then k, then v) when they are too many for the ring. A loader warp
+// brings whole tokens into a ring in shared memory with bulk copies, several
+// ahead, so that the loads of every SM stay in flight while the consumers
+// compute: with the next token's rows in registers instead the kernel kept 20
+// KB per SM in flight and moved 4.1 TB/s.
 // D/16 lanes share a head's row; a lane holds two blocks of eight channels:
 // (8j, rope/2 + 8j), so that with the halves style both members of every pair
-// sit in one lane, and two neighbouring blocks where nothing turns. A thread
-// owns the same two rows (heads) of every token its CTA takes, so the norm
-// weights stay in registers, a token's angles serve both rows, and the next
-// token's rows are loaded while this one's are computed: the kernel moves each
-// byte once and is bound by HBM (see launch_append_t for the shape).
+// sit in one lane, and two neighbouring blocks where nothing turns.
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(256) paged_append_kernel(const AppendPagedParams p) {
-    constexpr int LPR = D / 16;         // lanes per row
-    constexpr int NP = kAppendRows;     // rows per thread
+__global__ void __launch_bounds__(kAppendThreads + 32, 2) paged_append_kernel(const AppendPagedParams p) {
+    constexpr int LPR = D / 16;                    // lanes per row
+    constexpr int RPP = kAppendThreads / LPR;      // rows per pass
+    extern __shared__ __align__(128) uint8_t sm_append[];
+    __shared__ uint64_t full[kAppendStages], empty[kAppendStages];
+    __shared__ AppendToken token[kAppendStages];
+    __shared__ int abort_flag_s;
+    volatile int *abort_flag = &abort_flag_s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = p.Hq + 2 * p.Hkv;
+    const int h_lo = (int)((int64_t)H * blockIdx.y / gridDim.y), h_hi = (int)((int64_t)H * (blockIdx.y + 1) / gridDim.y);
+    const int rows = h_hi - h_lo, R = p.rope;
+    uint8_t *wq_s = sm_append, *wk_s = wq_s + 2 * D;   // norm weights
+    uint8_t *ring = wk_s + 2 * D;                      // stages: rows, then cosines and sines
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), kAppendThreads / 32);
+        }
+        abort_flag_s = 0;
+        fence_mbar_init();
+    }
     pdl_wait_and_release();
-    const int rpp = (int)blockDim.x / LPR;  // rows per pass
+    if ((int)threadIdx.x < D / 8) {
+        if (p.q_weight) reinterpret_cast<uint4 *>(wq_s)[threadIdx.x] = reinterpret_cast<const uint4 *>(p.q_weight)[threadIdx.x];
+        if (p.k_weight) reinterpret_cast<uint4 *>(wk_s)[threadIdx.x] = reinterpret_cast<const uint4 *>(p.k_weight)[threadIdx.x];
+    }
+    __syncthreads();
+    const int step = (int)gridDim.x, n_tok = (p.T - (int)blockIdx.x + step - 1) / step;
+
+    if (warp == kAppendThreads / 32) {
+        // ---- loader: 32 tokens' slots and positions at a time, a lane each ----
+        // rows of q, k and v in this CTA's range: [lo, hi) of each tensor
+        const int q_lo = min(h_lo, p.Hq), q_hi = min(h_hi, p.Hq);
+        const int k_lo = min(max(h_lo - p.Hq, 0), p.Hkv), k_hi = min(max(h_hi - p.Hq, 0), p.Hkv);
+        const int v_lo = max(h_lo - p.Hq - p.Hkv, 0), v_hi = max(h_hi - p.Hq - p.Hkv, 0);
+        const uint32_t bytes = (uint32_t)(rows * D * 2 + 4 * R);
+        int s = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        int issued = 0;
+        for (int i0 = 0; i0 < n_tok && ok; i0 += 32) {
+            int my_slot = -1, my_pos = 0;
+            if (i0 + lane < n_tok) {
+                const int t = (int)blockIdx.x + (i0 + lane) * step;
+                my_slot = p.slots[t];
+                if (R > 0) my_pos = p.positions[t];
+                int flags = 0;
+                if (my_slot >= 0) {
+                    if ((my_slot >> p.shift) >= p.num_pages) flags |= GQAQ_DEV_BAD_PAGE;
+                    if (R > 0 && (my_pos < 0 || my_pos >= p.max_position)) flags |= GQAQ_DEV_BAD_POS;
+                }
+                if (flags) {
+                    my_slot = -1;
+                    if (blockIdx.y == 0) raise_flag(p.status, flags);
+                }
+            }
+            for (int i = i0; i < min(i0 + 32, n_tok); ++i) {
+                const int slot = __shfl_sync(0xffffffffu, my_slot, i - i0), pos = __shfl_sync(0xffffffffu, my_pos, i - i0);
+                if (lane == 0) {
+                    const int64_t t = (int64_t)blockIdx.x + (int64_t)i * step;
+                    if (i >= p.stages) ok = mbar_wait(smem_u32(&empty[s]), ph, p.timeout_ns, abort_flag);
+                    if (ok) {
+                        token[s].slot = slot;
+                        const uint32_t fb = smem_u32(&full[s]);
+                        if (slot < 0) {
+                            mbar_arrive(fb);
+                        } else {
+                            mbar_arrive_expect_tx(fb, bytes);
+                            uint32_t dst = smem_u32(ring) + (uint32_t)s * (uint32_t)p.stage_bytes;
+                            auto bulk = [&](const void *src, uint32_t n) {
+                                if (n == 0) return;
+                                bulk_load(dst, src, n, fb);
+                                dst += n;
+                            };
+                            bulk(p.q + t * p.q_stride + q_lo * D, (uint32_t)(q_hi - q_lo) * D * 2);
+                            bulk(p.k + t * p.k_stride + k_lo * D, (uint32_t)(k_hi - k_lo) * D * 2);
+                            bulk(p.v + t * p.v_stride + v_lo * D, (uint32_t)(v_hi - v_lo) * D * 2);
+                            bulk(p.cos_sin + (int64_t)pos * R, (uint32_t)(4 * R));
+                        }
+                        ++issued;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (++s == p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            raise_flag(p.status, GQAQ_DEV_TIMEOUT);
+            *abort_flag = 1;
+            // let every copy already issued land before this CTA may retire
+            for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+                mbar_wait(smem_u32(&full[i % p.stages]), (uint32_t)(i / p.stages) & 1u, p.timeout_ns, nullptr);
+        }
+        return;
+    }
+
+    // ---- consumers ----
     const int j = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
-    const int R = p.rope;
     const bool turns = 16 * j < R;
     const int c0 = turns ? 8 * j : 16 * j, c1 = turns ? R / 2 + 8 * j : 16 * j + 8;
     // halves: pair i of both blocks is channel 8j + i; adjacent pairs: a block
     // of eight channels holds pairs c/2 .. c/2 + 3
     const int i0 = INTER ? c0 / 2 : 8 * j, i1 = INTER ? c1 / 2 : 8 * j + 4;
-    const int H = p.Hq + 2 * p.Hkv;
-    int head[NP], kind[NP];             // head within its tensor; 0 q, 1 k, 2 v, 3 none
-    uint4 wa[NP], wb[NP];
-    bool norm[NP];
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const int h = ((int)blockIdx.y * NP + n) * rpp + r0;
-        kind[n] = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : h < H ? 2 : 3;
-        head[n] = kind[n] == 0 ? h : kind[n] == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
-        const uint16_t *w = kind[n] == 0 ? p.q_weight : kind[n] == 1 ? p.k_weight : nullptr;
-        norm[n] = w != nullptr;
-        wa[n] = wb[n] = make_uint4(0u, 0u, 0u, 0u);
-        if (norm[n]) {
-            wa[n] = *reinterpret_cast<const uint4 *>(w + c0);
-            wb[n] = *reinterpret_cast<const uint4 *>(w + c1);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n_tok; ++i) {
+        if (!mbar_wait(smem_u32(&full[s]), ph, p.timeout_ns, abort_flag)) {
+            if (lane == 0) {
+                raise_flag(p.status, GQAQ_DEV_TIMEOUT);
+                *abort_flag = 1;
+            }
+            return;
         }
-    }
-    // a token's place, or -1: padding, or refused
-    auto place = [&](int t, int &pos) {
-        const int slot = p.slots[t];
-        pos = R > 0 ? p.positions[t] : 0;
-        int flags = 0;
-        if (slot < 0) return -1;
-        if ((slot >> p.shift) >= p.num_pages) flags |= GQAQ_DEV_BAD_PAGE;
-        if (R > 0 && (pos < 0 || pos >= p.max_position)) flags |= GQAQ_DEV_BAD_POS;
-        if (flags == 0) return slot;
-        if (threadIdx.x == 0 && blockIdx.y == 0) raise_flag(p.status, flags);
-        return -1;
-    };
-    auto load = [&](int t, uint4 (&x0)[NP], uint4 (&x1)[NP]) {
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            if (kind[n] == 3) continue;
-            const uint16_t *src = (kind[n] == 0 ? p.q + t * p.q_stride : kind[n] == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + head[n] * D;
-            x0[n] = *reinterpret_cast<const uint4 *>(src + c0);
-            x1[n] = *reinterpret_cast<const uint4 *>(src + c1);
-        }
-    };
-    uint4 x0[NP], x1[NP], y0[NP], y1[NP];
-#pragma unroll
-    for (int n = 0; n < NP; ++n) x0[n] = x1[n] = y0[n] = y1[n] = make_uint4(0u, 0u, 0u, 0u);
-    int pos = 0, next_pos = 0;
-    int slot = place(blockIdx.x, pos);
-    if (slot >= 0) load(blockIdx.x, x0, x1);
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int tn = t + (int)gridDim.x;
-        int next = -1;
-        if (tn < p.T) {
-            next = place(tn, next_pos);
-            if (next >= 0) load(tn, y0, y1);
-        }
-        if (slot >= 0) {  // the same for the whole CTA
-            float cs[8], sn[8];
+        const int slot = token[s].slot;
+        if (slot >= 0) {
+            const int64_t t = (int64_t)blockIdx.x + (int64_t)i * step;
+            const uint8_t *stage = ring + s * p.stage_bytes;
+            f32x2 cs[4], sn[4];
             if (turns) {
-                const float *row = p.cos_sin + (int64_t)pos * R;
+                const float *row = reinterpret_cast<const float *>(stage + rows * D * 2);
                 const float4 a = *reinterpret_cast<const float4 *>(row + i0), b = *reinterpret_cast<const float4 *>(row + i1);
                 const float4 c = *reinterpret_cast<const float4 *>(row + R / 2 + i0), d = *reinterpret_cast<const float4 *>(row + R / 2 + i1);
-                cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w; cs[4] = b.x; cs[5] = b.y; cs[6] = b.z; cs[7] = b.w;
-                sn[0] = c.x; sn[1] = c.y; sn[2] = c.z; sn[3] = c.w; sn[4] = d.x; sn[5] = d.y; sn[6] = d.z; sn[7] = d.w;
+                cs[0] = pair32(a.x, a.y); cs[1] = pair32(a.z, a.w); cs[2] = pair32(b.x, b.y); cs[3] = pair32(b.z, b.w);
+                sn[0] = pair32(c.x, c.y); sn[1] = pair32(c.z, c.w); sn[2] = pair32(d.x, d.y); sn[3] = pair32(d.z, d.w);
             }
             const int page = slot >> p.shift, row_in = slot & (p.S - 1);
+            // whole passes, so that the shuffles see all lanes of a row's group
+            for (int rb = 0; rb < rows; rb += RPP) {
+                const int rl = rb + r0;
+                const bool live = rl < rows;
+                const int h = h_lo + rl;
+                const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+                uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+                if (live) {
+                    x0 = *reinterpret_cast<const uint4 *>(stage + (rl * D + c0) * 2);
+                    x1 = *reinterpret_cast<const uint4 *>(stage + (rl * D + c1) * 2);
+                }
+                f32x2 a[4], b[4];
+                unpack8<BF16>(x0, a);
+                unpack8<BF16>(x1, b);
+                f32x2 sq = mul2(a[0], a[0]);
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                float a[8], b[8];
-                unpack8<BF16>(x0[n], a);
-                unpack8<BF16>(x1[n], b);
-                float ss = 0.f;
+                for (int e = 1; e < 4; ++e) sq = fma2(a[e], a[e], sq);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+                for (int e = 0; e < 4; ++e) sq = fma2(b[e], b[e], sq);
+                float ss = unpair32(sq).x + unpair32(sq).y;
 #pragma unroll
                 for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (kind[n] == 3) continue;
-                if (norm[n]) {
+                if (!live) continue;
+                const bool norm = !is_v && (is_q ? p.q_weight : p.k_weight) != nullptr;
+                if (norm) {
                     const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-                    float u[8], v[8];
-                    unpack8<BF16>(wa[n], u);
-                    unpack8<BF16>(wb[n], v);
+                    const f32x2 inv2 = pair32(inv, inv);
+                    const uint8_t *w = is_q ? wq_s : wk_s;
+                    f32x2 u[4], v[4];
+                    unpack8<BF16>(*reinterpret_cast<const uint4 *>(w + c0 * 2), u);
+                    unpack8<BF16>(*reinterpret_cast<const uint4 *>(w + c1 * 2), v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        a[e] = a[e] * inv * u[e];
-                        b[e] = b[e] * inv * v[e];
+                    for (int e = 0; e < 4; ++e) {
+                        a[e] = mul2(mul2(a[e], inv2), u[e]);
+                        b[e] = mul2(mul2(b[e], inv2), v[e]);
                     }
                 }
-                const bool turn = turns && kind[n] != 2;
+                const bool turn = turns && !is_v;
                 if (turn) {
                     if (INTER) {
+                        // (x, y) -> (x cos - y sin, y cos + x sin), a pair of channels per register pair
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float u = a[2 * e], v = a[2 * e + 1], y = b[2 * e], z = b[2 * e + 1];
-                            a[2 * e] = u * cs[e] - v * sn[e];
-                            a[2 * e + 1] = v * cs[e] + u * sn[e];
-                            b[2 * e] = y * cs[4 + e] - z * sn[4 + e];
-                            b[2 * e + 1] = z * cs[4 + e] + y * sn[4 + e];
+                            const float2 xa = unpair32(a[e]), xb = unpair32(b[e]);
+                            const float2 ca = unpair32(cs[e >> 1]), sa = unpair32(sn[e >> 1]);
+                            const float2 cb = unpair32(cs[2 + (e >> 1)]), sb = unpair32(sn[2 + (e >> 1)]);
+                            const float c = (e & 1) ? ca.y : ca.x, d = (e & 1) ? sa.y : sa.x;
+                            const float f = (e & 1) ? cb.y : cb.x, g = (e & 1) ? sb.y : sb.x;
+                            a[e] = fma2(pair32(-xa.y, xa.x), pair32(d, d), mul2(a[e], pair32(c, c)));
+                            b[e] = fma2(pair32(-xb.y, xb.x), pair32(g, g), mul2(b[e], pair32(f, f)));
                         }
                     } else {
+                        const f32x2 minus = pair32(-1.f, -1.f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float u = a[e], v = b[e];
-                            a[e] = u * cs[e] - v * sn[e];
-                            b[e] = v * cs[e] + u * sn[e];
+                        for (int e = 0; e < 4; ++e) {
+                            const f32x2 u = a[e], v = b[e];
+                            a[e] = fma2(mul2(v, minus), sn[e], mul2(u, cs[e]));
+                            b[e] = fma2(u, sn[e], mul2(v, cs[e]));
                         }
                     }
                 }
-                uint16_t *dst = kind[n] == 0 ? p.q_out + ((int64_t)t * p.Hq + head[n]) * D
-                                             : (kind[n] == 1 ? p.k_pages : p.v_pages) + (((int64_t)page * p.Hkv + head[n]) * p.S + row_in) * D;
-                const bool same = !norm[n] && !turn;  // nothing computed: the bits as they are
-                *reinterpret_cast<uint4 *>(dst + c0) = same ? x0[n] : pack8<BF16>(a);
-                *reinterpret_cast<uint4 *>(dst + c1) = same ? x1[n] : pack8<BF16>(b);
+                if (norm || turn) {  // else the bits as they are
+                    x0 = pack8<BF16>(a);
+                    x1 = pack8<BF16>(b);
+                }
+                const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+                uint16_t *dst = is_q ? p.q_out + (t * p.Hq + h) * D
+                                     : (is_v ? p.v_pages : p.k_pages) + (((int64_t)page * p.Hkv + hk) * p.S + row_in) * D;
+                *reinterpret_cast<uint4 *>(dst + c0) = x0;
+                *reinterpret_cast<uint4 *>(dst + c1) = x1;
             }
         }
-        slot = next;
-        pos = next_pos;
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            x0[n] = y0[n];
-            x1[n] = y1[n];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
+        if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
         }
     }
 }
 
 template <int D, bool BF16>
-int launch_append_t(const AppendPagedParams &p, bool inter, const LaunchCtx &ctx) {
+int launch_append_t(AppendPagedParams &p, bool inter, const LaunchCtx &ctx) {
     auto kern = inter ? paged_append_kernel<D, BF16, true> : paged_append_kernel<D, BF16, false>;
-    const int H = p.Hq + 2 * p.Hkv, lanes = D / 16;
-    // threads for half a token's rows (two rows each), in whole warps; more
-    // heads than 256 threads hold take more CTAs per token
-    int threads = ((H + kAppendRows - 1) / kAppendRows * lanes + 31) / 32 * 32;
-    if (threads > 256) threads = 256;
-    const int rows = threads / lanes * kAppendRows, gy = (H + rows - 1) / rows;
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) return GQAQ_ERR_CUDA;
-    int gx = per_sm * ctx.num_sms / gy;
+    // A token's rows are split over gy CTAs until two of them fit the ring.
+    const int H = p.Hq + 2 * p.Hkv, angles = 4 * p.rope;
+    int gy = 1;
+    auto stage = [&](int n) { return (H + n - 1) / n * D * 2 + angles; };
+    while (2 * stage(gy) > kAppendRing) ++gy;
+    p.stage_bytes = stage(gy);
+    p.stages = kAppendRing / p.stage_bytes < kAppendStages ? kAppendRing / p.stage_bytes : kAppendStages;
+    const size_t smem = 4 * D + (size_t)p.stages * p.stage_bytes;
+    static bool ready[2][64] = {};
+    if (ctx.device < 0 || ctx.device >= 64) return GQAQ_ERR_UNSUPPORTED;
+    if (!ready[inter][ctx.device]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * D + kAppendRing) != cudaSuccess)
+            return GQAQ_ERR_CUDA;
+        ready[inter][ctx.device] = true;
+    }
+    int gx = 2 * ctx.num_sms / gy;
     gx = gx < 1 ? 1 : gx < p.T ? gx : p.T;
-    const cudaError_t e = launch_kernel(kern, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)threads), 0, ctx, 0, p);
+    const cudaError_t e = launch_kernel(kern, dim3((unsigned)gx, (unsigned)gy), dim3(kAppendThreads + 32), smem, ctx, 0, p);
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;
 }
 
@@ -509,6 +614,7 @@ int launch_paged_append(const PagedAppendArgs &a, const LaunchCtx &ctx) {
     p.num_pages = d.num_pages;
     p.rope = a.rope_dim;
     p.max_position = a.max_position;
+    p.timeout_ns = ctx.timeout_ns;
     const bool inter = a.interleaved != 0;
     if (d.dtype == GQAQ_BF16)
         return d.head_dim == 128 ? launch_append_t<128, true>(p, inter, ctx) : launch_append_t<64, true>(p, inter, ctx);
