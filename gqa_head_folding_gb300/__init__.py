@@ -19,6 +19,7 @@ paged_release_pages, paged_norm_rope_append, gqa_paged_attn).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -698,32 +699,57 @@ def new_pages(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, 
     return torch.empty(num_pages, num_kv_heads, page_size, head_dim, dtype=dtype, device=device)
 
 
-def _paged(name: str, t, dtype, shape):
-    """A contiguous CUDA tensor of this dtype and shape on the current device (None in shape: any extent)."""
+def _paged_bad(name: str, t, dtype, shape, dev: int):
+    """Say what _paged found wrong with an argument."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    got = t.shape
-    if len(got) != len(shape):
-        raise ValueError(f"{name} must have {len(shape)} dims, got {tuple(got)}")
-    for have, want in zip(got, shape):
-        if want is not None and have != want:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _paged(name: str, t, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this dtype and shape on the current device."""
+    if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
+        _paged_bad(name, t, dtype, shape, dev)
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _paged_bad(name, t, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _paged_stream(*tensors) -> int:
-    """The current stream of the current device, which must hold every tensor."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got {t.device}")
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _paged_dim(name: str, t, ndim: int):
+    """The shape of a tensor argument of ndim dims."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _paged_device(name: str, t) -> int:
+    """The current device, which must hold t (and with it every other argument)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if dev != _cuda_device():
+        raise ValueError(f"{name} must be on the current device, got {t.device}")
+    return dev
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_dims_ref(*fields):
+    """A pointer to the gqaq_paged_dims with these fields (the library only reads it during the call)."""
+    return ctypes.pointer(PagedDims(*fields))
+
+
+_cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_cuda_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def paged_build_tables(cache_len, new_len, free_pages, free_count, block_table, max_tokens: int,
@@ -735,23 +761,30 @@ def paged_build_tables(cache_len, new_len, free_pages, free_count, block_table, 
     Requests are served in order, each wholly or not at all; a refused one has kv_len 0 and slots -1.
     free_count_out may be free_count itself; without it a new tensor holds the count."""
     i32 = torch.int32
-    B = cache_len.shape[0] if cache_len.dim() == 1 else -1
-    T = int(max_tokens)
-    dev = cache_len.device
-    kv_len = torch.empty(B, dtype=i32, device=dev) if kv_len is None else kv_len
-    cu_q = torch.empty(B + 1, dtype=i32, device=dev) if cu_q is None else cu_q
-    positions = torch.empty(T, dtype=i32, device=dev) if positions is None else positions
-    slots = torch.empty(T, dtype=i32, device=dev) if slots is None else slots
-    free_count_out = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
-    args = (_paged("cache_len", cache_len, i32, (None,)), _paged("new_len", new_len, i32, (B,)),
-            _paged("free_pages", free_pages, i32, (None,)), _paged("free_count", free_count, i32, (1,)),
-            _paged("block_table", block_table, i32, (B, None)), _paged("kv_len", kv_len, i32, (B,)),
-            _paged("cu_q", cu_q, i32, (B + 1,)), _paged("positions", positions, i32, (T,)),
-            _paged("slots", slots, i32, (T,)), _paged("free_count_out", free_count_out, i32, (1,)))
-    d = PagedDims(B, 0, 0, 0, int(page_size), free_pages.shape[0], block_table.shape[1], T, 0)
-    stream = _paged_stream(cache_len, new_len, free_pages, free_count, block_table, kv_len, cu_q, positions, slots,
-                           free_count_out)
-    _check("paged_build_tables", lib().paged_build_tables(ctypes.byref(d), *args, stream))
+    (B,) = _paged_dim("cache_len", cache_len, 1)
+    dev = _paged_device("cache_len", cache_len)
+    _, width = _paged_dim("block_table", block_table, 2)
+    (pool,) = _paged_dim("free_pages", free_pages, 1)
+    T, per_b, per_t, one = int(max_tokens), (B,), (int(max_tokens),), (1,)
+    if kv_len is None:
+        kv_len = torch.empty(per_b, dtype=i32, device=cache_len.device)
+    if cu_q is None:
+        cu_q = torch.empty(B + 1, dtype=i32, device=cache_len.device)
+    if positions is None:
+        positions = torch.empty(per_t, dtype=i32, device=cache_len.device)
+    if slots is None:
+        slots = torch.empty(per_t, dtype=i32, device=cache_len.device)
+    if free_count_out is None:
+        free_count_out = torch.empty(one, dtype=i32, device=cache_len.device)
+    status = lib().paged_build_tables(
+        _paged_dims_ref(B, 0, 0, 0, int(page_size), pool, width, T, 0),
+        _paged("cache_len", cache_len, i32, per_b, dev), _paged("new_len", new_len, i32, per_b, dev),
+        _paged("free_pages", free_pages, i32, (pool,), dev), _paged("free_count", free_count, i32, one, dev),
+        _paged("block_table", block_table, i32, (B, width), dev), _paged("kv_len", kv_len, i32, per_b, dev),
+        _paged("cu_q", cu_q, i32, (B + 1,), dev), _paged("positions", positions, i32, per_t, dev),
+        _paged("slots", slots, i32, per_t, dev), _paged("free_count_out", free_count_out, i32, one, dev),
+        _cuda_stream(dev))
+    _check("paged_build_tables", status)
     return kv_len, cu_q, positions, slots, free_count_out
 
 
@@ -760,33 +793,31 @@ def paged_release_pages(kv_len, keep_len, block_table, free_pages, free_count, p
     """Append the pages past keep_len [B] of kv_len [B] tokens to free_pages behind its first free_count
     entries; returns the new count (free_count_out, which may be free_count itself)."""
     i32 = torch.int32
-    free_count_out = torch.empty(1, dtype=i32, device=free_count.device) if free_count_out is None else free_count_out
-    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    args = (_paged("kv_len", kv_len, i32, (None,)), _paged("keep_len", keep_len, i32, (B,)),
-            _paged("block_table", block_table, i32, (B, None)), _paged("free_pages", free_pages, i32, (None,)),
-            _paged("free_count", free_count, i32, (1,)), _paged("free_count_out", free_count_out, i32, (1,)))
-    d = PagedDims(B, 0, 0, 0, int(page_size), free_pages.shape[0], block_table.shape[1], 1, 0)
-    stream = _paged_stream(kv_len, keep_len, block_table, free_pages, free_count, free_count_out)
-    _check("paged_release_pages", lib().paged_release_pages(ctypes.byref(d), *args, stream))
+    (B,) = _paged_dim("kv_len", kv_len, 1)
+    dev = _paged_device("kv_len", kv_len)
+    _, width = _paged_dim("block_table", block_table, 2)
+    (pool,) = _paged_dim("free_pages", free_pages, 1)
+    if free_count_out is None:
+        free_count_out = torch.empty(1, dtype=i32, device=kv_len.device)
+    status = lib().paged_release_pages(
+        _paged_dims_ref(B, 0, 0, 0, int(page_size), pool, width, 1, 0),
+        _paged("kv_len", kv_len, i32, (B,), dev), _paged("keep_len", keep_len, i32, (B,), dev),
+        _paged("block_table", block_table, i32, (B, width), dev), _paged("free_pages", free_pages, i32, (pool,), dev),
+        _paged("free_count", free_count, i32, (1,), dev), _paged("free_count_out", free_count_out, i32, (1,), dev),
+        _cuda_stream(dev))
+    _check("paged_release_pages", status)
     return free_count_out
 
 
-def _paged_rows(name: str, t, dtype, T: int, H, D: int):
-    """[T,H,D] rows whose heads are contiguous; returns (pointer, elements between tokens)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or t.shape[2] != D:
-        raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
+def _paged_rows(name: str, t, dtype, shape, dev: int):
+    """(address, elements between tokens) of [T,H,D] rows whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _paged_bad(name, t, dtype, shape, dev)
+    T, H, D = shape
     st, sh, sd = t.stride()
     if sd != 1 or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {(st, sh, sd)}")
-    if T == 1:
-        st = H * D  # a single token: whatever the stride says
-    return t.data_ptr(), st
+    return t.data_ptr(), st if T > 1 else H * D  # a single token: whatever the stride says
 
 
 def paged_norm_rope_append(q, k, v, positions, slots, k_pages, v_pages, q_weight=None, k_weight=None,
@@ -796,31 +827,31 @@ def paged_norm_rope_append(q, k, v, positions, slots, k_pages, v_pages, q_weight
     q_out [T,Hq,D], k and v to row slots[t] of the pages [num_pages,Hkv,S,D]. Tokens with slots[t] < 0
     are padding. q, k and v may be slices of one fused projection (heads contiguous, any token stride
     that is a multiple of 8). Returns q_out."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a tensor of shape [T,Hq,D]")
+    i32 = torch.int32
+    T, Hq, D = _paged_dim("q", q, 3)
+    dev = _paged_device("q", q)
+    pool = _paged_dim("k_pages", k_pages, 4)
+    num_pages, Hkv, S, _ = pool
     dt = q.dtype
-    T, Hq, D = q.shape
-    pk = _paged("k_pages", k_pages, dt, (None, None, None, D))
-    num_pages, Hkv, S, _ = k_pages.shape
-    pv = _paged("v_pages", v_pages, dt, (num_pages, Hkv, S, D))
-    q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device) if q_out is None else q_out
-    (aq, sq), (ak, sk), (av, sv) = (_paged_rows("q", q, dt, T, Hq, D), _paged_rows("k", k, dt, T, Hkv, D),
-                                    _paged_rows("v", v, dt, T, Hkv, D))
-    ao = _paged("q_out", q_out, dt, (T, Hq, D))
-    apos, aslot = _paged("positions", positions, torch.int32, (T,)), _paged("slots", slots, torch.int32, (T,))
-    wq = None if q_weight is None else _paged("q_weight", q_weight, dt, (D,))
-    wk = None if k_weight is None else _paged("k_weight", k_weight, dt, (D,))
-    cs, rope, most = None, 0, 0
-    if cos_sin is not None:
-        cs = _paged("cos_sin", cos_sin, torch.float32, (None, None))
-        most, rope = cos_sin.shape
     if dt not in _PAGED_DTYPES:
         raise ValueError(f"q must be torch.float16 or torch.bfloat16, got {dt}")
-    d = PagedDims(1, Hq, Hkv, D, S, num_pages, 1, T, _PAGED_DTYPES[dt])
-    stream = _paged_stream(q, k, v, positions, slots, k_pages, v_pages, q_weight, k_weight, cos_sin, q_out)
-    _check("paged_norm_rope_append", lib().paged_norm_rope_append(
-        ctypes.byref(d), aq, sq, ak, sk, av, sv, apos, aslot, wq, wk, eps, cs, rope, most, 1 if interleaved else 0, ao, pk,
-        pv, stream))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    (aq, sq), (ak, sk), (av, sv) = (_paged_rows("q", q, dt, (T, Hq, D), dev), _paged_rows("k", k, dt, (T, Hkv, D), dev),
+                                    _paged_rows("v", v, dt, (T, Hkv, D), dev))
+    cs, rope, most = None, 0, 0
+    if cos_sin is not None:
+        most, rope = _paged_dim("cos_sin", cos_sin, 2)
+        cs = _paged("cos_sin", cos_sin, torch.float32, (most, rope), dev)
+    status = lib().paged_norm_rope_append(
+        _paged_dims_ref(1, Hq, Hkv, D, S, num_pages, 1, T, _PAGED_DTYPES[dt]), aq, sq, ak, sk, av, sv,
+        _paged("positions", positions, i32, (T,), dev), _paged("slots", slots, i32, (T,), dev),
+        None if q_weight is None else _paged("q_weight", q_weight, dt, (D,), dev),
+        None if k_weight is None else _paged("k_weight", k_weight, dt, (D,), dev), eps, cs, rope, most,
+        1 if interleaved else 0, _paged("q_out", q_out, dt, (T, Hq, D), dev),
+        _paged("k_pages", k_pages, dt, (num_pages, Hkv, S, D), dev), _paged("v_pages", v_pages, dt, pool, dev),
+        _cuda_stream(dev))
+    _check("paged_norm_rope_append", status)
     return q_out
 
 
@@ -830,26 +861,26 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, cu_q, kv_len, scale: float,
     cu_q[b]..cu_q[b+1]-1, the last of its kv_len[b] tokens), pages [num_pages,Hkv,S,D], block_table
     [B,max_pages]; every token attends to the tokens up to itself. max_q_len bounds the rows of a
     request. Rows of out outside the requests' are left as they were."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a tensor of shape [T,Hq,D]")
-    dt = q.dtype
-    T, Hq, D = q.shape
-    aq = _paged("q", q, dt, (T, Hq, D))
-    pk = _paged("k_pages", k_pages, dt, (None, None, None, D))
-    num_pages, Hkv, S, _ = k_pages.shape
-    pv = _paged("v_pages", v_pages, dt, (num_pages, Hkv, S, D))
-    tab = _paged("block_table", block_table, torch.int32, (None, None))
-    B, max_pages = block_table.shape
-    acu, alen = _paged("cu_q", cu_q, torch.int32, (B + 1,)), _paged("kv_len", kv_len, torch.int32, (B,))
+    i32 = torch.int32
+    rows = _paged_dim("q", q, 3)
+    dev = _paged_device("q", q)
+    T, Hq, D = rows
+    num_pages, Hkv, S, _ = _paged_dim("k_pages", k_pages, 4)
+    B, max_pages = _paged_dim("block_table", block_table, 2)
+    dt, pool = q.dtype, (num_pages, Hkv, S, D)
     if dt not in _PAGED_DTYPES:
         raise ValueError(f"q must be torch.float16 or torch.bfloat16, got {dt}")
-    d = PagedDims(B, Hq, Hkv, D, S, num_pages, max_pages, T, _PAGED_DTYPES[dt])
-    out = torch.empty_like(q) if out is None else out
-    ao = _paged("out", out, dt, (T, Hq, D))
+    aq = _paged("q", q, dt, rows, dev)
+    dims = _paged_dims_ref(B, Hq, Hkv, D, S, num_pages, max_pages, T, _PAGED_DTYPES[dt])
+    if out is None:
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = alloc_paged_workspace(d, q.device)
-    aws = _paged("workspace", workspace, torch.uint8, (None,))
-    stream = _paged_stream(q, k_pages, v_pages, block_table, cu_q, kv_len, out, workspace)
-    _check("gqa_paged_attn", lib().gqa_paged_attn(
-        ctypes.byref(d), max_q_len, aq, pk, pv, tab, acu, alen, scale, ao, aws, workspace.shape[0], stream))
+        workspace = alloc_paged_workspace(dims.contents, q.device)
+    (nbytes,) = _paged_dim("workspace", workspace, 1)
+    status = lib().gqa_paged_attn(
+        dims, max_q_len, aq, _paged("k_pages", k_pages, dt, pool, dev), _paged("v_pages", v_pages, dt, pool, dev),
+        _paged("block_table", block_table, i32, (B, max_pages), dev), _paged("cu_q", cu_q, i32, (B + 1,), dev),
+        _paged("kv_len", kv_len, i32, (B,), dev), scale, _paged("out", out, dt, rows, dev),
+        _paged("workspace", workspace, torch.uint8, (nbytes,), dev), nbytes, _cuda_stream(dev))
+    _check("gqa_paged_attn", status)
     return out

@@ -3,6 +3,8 @@
 // layer's projection and its attention (per-head RMS norm, rotation, append).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace gqaq {
@@ -285,10 +287,12 @@ __device__ __forceinline__ uint4 pack8(const f32x2 (&y)[4]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Bytes of shared memory a CTA's ring of tokens may take (two CTAs per SM).
-constexpr int kAppendRing = 96 * 1024;
+// Bytes of shared memory of a CTA's ring of tokens. Three CTAs per SM whose
+// rings hold three tokens of 48 rows moved 8192 of them in 36 us (5.7 TB/s);
+// rings of 64 and 110 KB took 44 and 50 us.
+constexpr int kAppendRing = 40 * 1024;
 constexpr int kAppendStages = 6;        // tokens in flight at most
-constexpr int kAppendThreads = 256;     // consumer threads
+constexpr int kAppendThreads = 256;     // consumer threads at most
 
 // What the loader leaves beside a token's rows.
 struct alignas(16) AppendToken {
@@ -306,15 +310,15 @@ struct alignas(16) AppendToken {
 // (8j, rope/2 + 8j), so that with the halves style both members of every pair
 // sit in one lane, and two neighbouring blocks where nothing turns.
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads + 32, 2) paged_append_kernel(const AppendPagedParams p) {
+__global__ void __launch_bounds__(kAppendThreads + 32, 3) paged_append_kernel(const AppendPagedParams p) {
     constexpr int LPR = D / 16;                    // lanes per row
-    constexpr int RPP = kAppendThreads / LPR;      // rows per pass
     extern __shared__ __align__(128) uint8_t sm_append[];
     __shared__ uint64_t full[kAppendStages], empty[kAppendStages];
     __shared__ AppendToken token[kAppendStages];
     __shared__ int abort_flag_s;
     volatile int *abort_flag = &abort_flag_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int consumers = (int)blockDim.x - 32, rpp = consumers / LPR;  // threads, rows per pass
     const int H = p.Hq + 2 * p.Hkv;
     const int h_lo = (int)((int64_t)H * blockIdx.y / gridDim.y), h_hi = (int)((int64_t)H * (blockIdx.y + 1) / gridDim.y);
     const int rows = h_hi - h_lo, R = p.rope;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kAppendThreads + 32, 2) paged_append_kernel(co
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), kAppendThreads / 32);
+            mbar_init(smem_u32(&empty[s]), (uint32_t)consumers / 32);
         }
         abort_flag_s = 0;
         fence_mbar_init();
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kAppendThreads + 32, 2) paged_append_kernel(co
     __syncthreads();
     const int step = (int)gridDim.x, n_tok = (p.T - (int)blockIdx.x + step - 1) / step;
 
-    if (warp == kAppendThreads / 32) {
+    if (warp == consumers / 32) {
         // ---- loader: 32 tokens' slots and positions at a time, a lane each ----
         // rows of q, k and v in this CTA's range: [lo, hi) of each tensor
         const int q_lo = min(h_lo, p.Hq), q_hi = min(h_hi, p.Hq);
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kAppendThreads + 32, 2) paged_append_kernel(co
             }
             const int page = slot >> p.shift, row_in = slot & (p.S - 1);
             // whole passes, so that the shuffles see all lanes of a row's group
-            for (int rb = 0; rb < rows; rb += RPP) {
+            for (int rb = 0; rb < rows; rb += rpp) {
                 const int rl = rb + r0;
                 const bool live = rl < rows;
                 const int h = h_lo + rl;
@@ -536,9 +540,23 @@ int launch_append_t(AppendPagedParams &p, bool inter, const LaunchCtx &ctx) {
             return GQAQ_ERR_CUDA;
         ready[inter][ctx.device] = true;
     }
-    int gx = 2 * ctx.num_sms / gy;
+    // consumers: the rows in as few passes as 256 threads allow, all full
+    const int rows = (H + gy - 1) / gy, lanes = D / 16, passes = (rows * lanes + kAppendThreads - 1) / kAppendThreads;
+    const int threads = ((rows + passes - 1) / passes * lanes + 31) / 32 * 32 + 32;
+    // CTAs per SM, asked for once per shape (the driver's answer costs more than the launch)
+    static std::atomic<uint64_t> known[2][64] = {};
+    const uint64_t shape = ((uint64_t)smem << 32) | ((uint64_t)threads << 8);
+    uint64_t got = known[inter][ctx.device].load(std::memory_order_relaxed);
+    if ((got & ~0xffull) != shape) {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) return GQAQ_ERR_CUDA;
+        got = shape | (uint64_t)n;
+        known[inter][ctx.device].store(got, std::memory_order_relaxed);
+    }
+    const int per_sm = (int)(got & 0xffu);
+    int gx = per_sm * ctx.num_sms / gy;
     gx = gx < 1 ? 1 : gx < p.T ? gx : p.T;
-    const cudaError_t e = launch_kernel(kern, dim3((unsigned)gx, (unsigned)gy), dim3(kAppendThreads + 32), smem, ctx, 0, p);
+    const cudaError_t e = launch_kernel(kern, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)threads), smem, ctx, 0, p);
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;
 }
 
