@@ -28,7 +28,7 @@ namespace gqaq {
 namespace {
 
 constexpr int kRows = 8;          // rows of an item: q_len * G at most
-constexpr int kMinTiles = 4;      // tiles per CTA below which a small step uses fewer CTAs
+constexpr int kMinUnits = 4;      // tiles per CTA below which a small step uses fewer CTAs
 
 template <int D>
 struct PdCfg {
@@ -234,11 +234,11 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
         prefetch_tensormap(&vmap);
     }
     pdl_wait_and_release();
-    paged_schedule(p.w, sched, scratch, kMinTiles);
+    paged_schedule(p.w, sched, scratch, kMinUnits);
     if (warp < 8) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 256);
     if (sched->t_begin >= sched->t_end) return;
     PagedWalk w;
-    w.init(p.w, *sched);
+    if (!w.init(p.w, *sched)) return;
 
     if (warp == 8) {
         // ---- loader: a lane per page ----
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
                 if (t + 1 < n) row = row_of(w.local + t + 1);
             }
             if (!ok) break;
-        } while (w.next(w.seg_len(), p.w));
+        } while (w.advance(p.w));
         if (!ok && lane == 0) {
             raise_flag(p.status, GQAQ_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
 
         // ---- merge the eight warps' states, four rows at a time ----
         const int64_t out0 = ((int64_t)w.s.q0 * p.Hq + (w.kv << p.gshift)) * D;
-        float *part = p.part + ((int64_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * C::PART;
+        float *part = p.part + ((int64_t)blockIdx.x * 2 + w.slot()) * C::PART;
         for (int first = 0; first < rows; first += C::MROWS) {
             wa.store(merge + warp * C::MROWS * (D + 2), first);
             named_bar_sync(1, 256);
@@ -364,33 +364,30 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
             if (tid == 0) {
                 // the barrier above orders every thread's partial stores before this
                 // release; the last arrival acquires all of them
-                const int64_t c_lo = tile_owner(w.off, sched->T, sched->grid);
-                const int np = (int)(tile_owner(w.off + w.tiles - 1, sched->T, sched->grid) - c_lo) + 1;
-                const unsigned old = atomic_add_acq_rel_gpu(&p.count[c_lo], 1u);
+                const PagedParts parts(*sched, w.off, w.tiles, 0);
+                const unsigned old = atomic_add_acq_rel_gpu(&p.count[parts.lo], 1u);
                 PdSplit &sp = split[nsplit];
                 sp.off = w.off;
                 sp.out = out0;
                 sp.tiles = w.tiles;
                 sp.rows = rows;
-                sp.last = old + 1u == (unsigned)np;
-                if (sp.last) p.count[c_lo] = 0u;
+                sp.last = old + 1u == (unsigned)parts.n;
+                if (sp.last) p.count[parts.lo] = 0u;
             }
             ++nsplit;  // at most the first and the last segment of a range
         }
-    } while (w.next(w.seg_len(), p.w));
+    } while (w.advance(p.w));
 
     if (nsplit == 0) return;
     named_bar_sync(1, 256);  // thread 0's arrivals are recorded
     for (int k = 0; k < nsplit; ++k) {
         const PdSplit sp = split[k];
         if (!sp.last) continue;
-        const int64_t T = sched->T;
-        const int gp = sched->grid;
-        const int64_t c_lo = tile_owner(sp.off, T, gp);
-        const int np = (int)(tile_owner(sp.off + sp.tiles - 1, T, gp) - c_lo) + 1;
-        // partials: slot 0, but the first CTA's, whose slot is 1 unless the item begins its range
-        const float *base = p.part + c_lo * 2 * C::PART;
-        const float *p0 = base + (tile_begin(c_lo, T, gp) == sp.off ? 0 : C::PART);
+        const PagedParts parts(*sched, sp.off, sp.tiles, 0);
+        const int np = parts.n;
+        // partials: slot 0, but the first CTA's
+        const float *base = p.part + parts.lo * 2 * C::PART;
+        const float *p0 = base + parts.slot_lo * C::PART;
         for (int x = tid; x < sp.rows * D; x += 256) {
             const int rho = x / D, d = x - rho * D;
             const int at = rho * (D + 2);
@@ -442,7 +439,7 @@ int launch_decode(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (!encode_tensor_map_kpage(&vmap, a.v_pages, rows, D, d.page_size)) return GQAQ_ERR_CUDA;
     const int G = d.num_q_heads / d.num_kv_heads;
     PdParams p;
-    fill_paged_work(a, 23, p.w);  // one block: every token of a request
+    fill_paged_work(a, 23, 1 << 23, p.w);  // one block: every token of a request
     p.q = static_cast<const uint16_t *>(a.q);
     p.out = static_cast<uint16_t *>(a.out);
     p.count = reinterpret_cast<unsigned *>(a.workspace);

@@ -54,7 +54,7 @@ struct PtcCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-constexpr int kMinTiles = 2;        // tiles per CTA below which a small step uses fewer CTAs
+constexpr int kMinUnits = 2;        // units per CTA below which a small step uses fewer CTAs (two at least: see PagedParts)
 constexpr float kSumLimit = 32768.f;  // of 64 P: above it some P passes 2^9
 constexpr float kRefMove = 9.f;       // log2 of the P that moves a row's reference
 constexpr float kRefDrop = 6.f;       // the new reference's distance under the row's maximum
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     }
     pdl_wait_and_release();
     tc_fence_before();
-    paged_schedule(p.w, sched, scratch, kMinTiles);
+    paged_schedule(p.w, sched, scratch, kMinUnits);
     tc_fence_after();
     const uint32_t tbase = *tslot;
     if (warp < 16) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 512);
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             // Loaders: K (and Q) in warp 16, V in warp 18. A lane per page.
             // --------------------------------------------------------------
             PagedWalk w;
-            w.init(p.w, *sched);
+            bool more = w.init(p.w, *sched);
             const bool is_k = warp == 16;
             const int NS = is_k ? C::NK : C::NV;
             uint64_t *full = is_k ? kfull : vfull, *empty = is_k ? kempty : vempty;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             const int ppt = kPagedTile >> p.w.shift;
             int seg = 0, i = 0;
             bool ok = true;
-            do {
+            while (more) {
                 const int n = w.seg_len();
                 const int rows = min(TB, w.s.m - w.rb * TB) * p.G;
                 if (is_k) {
@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 }
                 if (!ok) break;
                 ++seg;
-            } while (w.next(w.seg_len(), p.w));
+                more = w.advance(p.w);
+            }
             if (!ok && lane == 0) {
                 raise_flag(p.status, GQAQ_DEV_TIMEOUT);
                 *abort_flag = 1;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             // runs one thread's MMAs in order.
             // --------------------------------------------------------------
             PagedWalk w;
-            w.init(p.w, *sched);
+            bool more = w.init(p.w, *sched);
             constexpr uint32_t IDESC_S = umma_idesc(128, 128, 0, BF16);
             constexpr uint32_t IDESC_O = umma_idesc(128, D, 1, BF16);
             const uint64_t qdesc0 = umma_desc(smem_u32(sq), 16);
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     if (e + 2 < ne) issue_s(e + 2);
                 }
             };
-            do {
+            while (more) {
                 const int n = w.seg_len();
                 const int rows = min(TB, w.s.m - w.rb * TB) * p.G;
                 ok = wait(qfull, sp);
@@ -394,7 +395,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 }
                 sp ^= 1u;
                 first_seg = false;
-            } while (ok && w.next(w.seg_len(), p.w));
+                more = ok && w.advance(p.w);
+            }
             if (!ok && lane == 0) {
                 raise_flag(p.status, GQAQ_DEV_TIMEOUT);
                 *abort_flag = 1;
@@ -411,10 +413,10 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             // every other barrier goes through.
             // --------------------------------------------------------------
             PagedWalk w;
-            w.init(p.w, *sched);
+            bool more = w.init(p.w, *sched);
             uint32_t sph = 0;
             bool ok = true;
-            do {
+            while (more) {
                 const int n = w.seg_len();
                 const int ne = min(TB, w.s.m - w.rb * TB) * p.G > 128 ? 2 * n : n;
                 for (int e = 0; e < ne; ++e) {
@@ -431,7 +433,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     tc_fence_before();
                     named_bar_sync(10 + x, 288);  // also after a timeout: the groups pass once per tile
                 }
-            } while (w.next(w.seg_len(), p.w));
+                more = w.advance(p.w);
+            }
         } else if (warp < 16) {
             // --------------------------------------------------------------
             // Softmax groups: two threads per row, tokens 64 h .. 64 h + 63 of
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             uint32_t oph = 0;  // phase of o_done
             bool ok = true;
             if (tid == 0) {
-                seg_s->w.init(p.w, *sched);
+                seg_s->more = seg_s->w.init(p.w, *sched);
                 seg_s->v_before = 0;
             }
             named_bar_sync(1, 512);
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 }
                 return r;
             };
-            do {
+            while (seg_s->more) {
                 const int n = w.seg_len();
                 const int rows = min(TB, w.s.m - w.rb * TB) * p.G;
                 const bool dual = rows > 128;
@@ -634,7 +637,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const bool second = !dual && n > 1;
                 const int q_row = w.s.q0 + w.rb * TB + (rho >> p.gshift);
                 uint16_t *dst = p.out + ((int64_t)q_row * p.Hq + w.kv * p.G + (rho & (p.G - 1))) * D;
-                const int slot = w.first ? 0 : 1;
+                const int slot = w.slot();
                 float *part = p.part + ((int64_t)blockIdx.x * 2 + slot) * C::PART;
                 if (warp_live) {
                     if (!whole && live && h == 0 && (dual || g == 0)) reinterpret_cast<float2 *>(part)[rho] = make_float2(M, L);
@@ -681,25 +684,22 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
 
                 if (!whole) {
                     // ---- arrive at the split item; the last arrival merges it ----
-                    const int64_t T = sched->T;
-                    const int gp = sched->grid;
-                    const int64_t c_lo = tile_owner(w.off, T, gp);
-                    const int np = (int)(tile_owner(w.off + w.tiles - 1, T, gp) - c_lo) + 1;
+                    const PagedParts parts(*sched, w.off, w.tiles, w.us);
+                    const int np = parts.n;
                     if (tid == 0) {
                         // the barrier orders every thread's partial stores before this
                         // release; the last arrival acquires all of them
-                        const unsigned old = atomic_add_acq_rel_gpu(&p.count[c_lo], 1u);
+                        const unsigned old = atomic_add_acq_rel_gpu(&p.count[parts.lo], 1u);
                         const int last = old + 1u == (unsigned)np;
-                        if (last) p.count[c_lo] = 0u;
+                        if (last) p.count[parts.lo] = 0u;
                         sched->last = last;
                     }
                     named_bar_sync(1, 512);
                     if (sched->last && live) {
                         // partials: slot 0 (a range's first segment), but the first CTA's,
                         // which is its last unless the item begins its range
-                        const int slot_lo = tile_begin(c_lo, T, gp) == w.off ? 0 : 1;
-                        const float *base = p.part + c_lo * 2 * C::PART;
-                        auto part_of = [&](int i) { return base + (int64_t)(2 * i + (i == 0 ? slot_lo : 0)) * C::PART; };
+                        const float *base = p.part + parts.lo * 2 * C::PART;
+                        auto part_of = [&](int i) { return base + (int64_t)(2 * i + (i == 0 ? parts.slot_lo : 0)) * C::PART; };
                         float mx = -INFINITY, sum = 0.f;
                         for (int i = 0; i < np; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + 2 * rho));
                         for (int i = 0; i < np; ++i) {
@@ -742,10 +742,10 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 named_bar_sync(1, 512);  // the segment has been read
                 if (tid == 0) {
                     seg_s->v_before += n;
-                    seg_s->more = seg_s->w.next(n, p.w);
+                    seg_s->more = seg_s->w.advance(p.w);
                 }
                 named_bar_sync(1, 512);
-            } while (seg_s->more);
+            }
         }
     }
 
@@ -771,7 +771,7 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     
     p.G = d.num_q_heads / d.num_kv_heads;
     p.gshift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3;
-    fill_paged_work(a, 8 - p.gshift, p.w);  // 256 rows
+    fill_paged_work(a, 8 - p.gshift, 128 >> p.gshift, p.w);  // blocks of 256 rows; above 128 a tile runs twice
     CUtensorMap qmap, kmap, vmap;
     if (!encode_tensor_map_heads(&qmap, a.q, d.max_tokens, d.num_q_heads, D, p.G, 128 / p.G)) return GQAQ_ERR_CUDA;
     if (!encode_tensor_map_2d(&kmap, a.k_pages, rows, D, 64, d.page_size, true)) return GQAQ_ERR_CUDA;

@@ -3,11 +3,13 @@
 // An item is (request, KV head, block of TB tokens); the G query heads of the
 // KV head and the block's tokens form its rows, token outer: row r is token
 // r / G, head r % G. An item's context is cut into tiles of 128 tokens, up to
-// its last row's position. The tiles of all items, in the order (request, KV
-// head, block, tile), are split into equal contiguous ranges, one per CTA, so
-// a batch of unlike lengths loads all SMs alike; consecutive CTAs work on the
-// same keys, which the L2 then serves. An item cut by a range boundary is
-// merged by the CTA that finishes last.
+// its last row's position. A tile costs one unit, or two where the block has
+// more than `half` tokens (the tensor-memory kernel runs it for two row
+// tiles). The units of all items, in the order (request, KV head, block,
+// tile), are split into equal contiguous ranges, one per CTA, so a batch of
+// unlike lengths loads all SMs alike; consecutive CTAs work on the same keys,
+// which the L2 then serves. A tile is its first unit's owner's. An item cut by
+// a range boundary is merged by the CTA that finishes last.
 #pragma once
 
 #include "internal.h"
@@ -21,11 +23,12 @@ struct PagedWorkParams {
     int B, T, Hkv, max_q;
     int shift;             // log2 of the page size
     int tbs;               // log2 of TB, the tokens per block
+    int half;              // tokens of a block above which its tiles cost two units
     int num_pages, max_pages;
     int64_t room;          // max_pages * page size
 };
 
-inline void fill_paged_work(const PagedAttnArgs &a, int tbs, PagedWorkParams &w) {
+inline void fill_paged_work(const PagedAttnArgs &a, int tbs, int half, PagedWorkParams &w) {
     const gqaq_paged_dims &d = *a.dims;
     w.table = a.block_table;
     w.cu_q = a.cu_q;
@@ -35,6 +38,7 @@ inline void fill_paged_work(const PagedAttnArgs &a, int tbs, PagedWorkParams &w)
     w.Hkv = d.num_kv_heads;
     w.max_q = a.max_q_len;
     w.tbs = tbs;
+    w.half = half;
     w.shift = 0;
     while ((1 << w.shift) < d.page_size) ++w.shift;
     w.num_pages = d.num_pages;
@@ -94,10 +98,20 @@ __device__ __forceinline__ int64_t tiles_before(const PagedSeq &s, int64_t rb, i
     return sum_ceil(u + n - 1, kPagedTileLog - tbs) - sum_ceil(u - 1, kPagedTileLog - tbs);
 }
 
-__device__ __forceinline__ int64_t head_tiles(const PagedSeq &s, int tbs) {
+// log2 of the units of a tile of block rb
+__device__ __forceinline__ int unit_shift(const PagedSeq &s, int rb, const PagedWorkParams &p) {
+    return s.m - (rb << p.tbs) > p.half ? 1 : 0;
+}
+
+// Units of the first rb blocks (each but a request's last is whole, hence of
+// one kind), and of all blocks of a head.
+__device__ __forceinline__ int64_t units_before(const PagedSeq &s, int rb, const PagedWorkParams &p) {
+    return tiles_before(s, rb, p.tbs) << unit_shift(s, 0, p);
+}
+__device__ __forceinline__ int64_t head_units(const PagedSeq &s, const PagedWorkParams &p) {
     if (s.m <= 0) return 0;
-    const int last = (s.m - 1) >> tbs;
-    return tiles_before(s, last, tbs) + block_tiles(s, last, tbs);
+    const int last = (s.m - 1) >> p.tbs;
+    return units_before(s, last, p) + ((int64_t)block_tiles(s, last, p.tbs) << unit_shift(s, last, p));
 }
 
 // Up to 64 probes of a barrier's phase in the shortest loop there is: a
@@ -143,50 +157,67 @@ __device__ __forceinline__ bool warp_mbar_wait_slow(uint32_t bar, uint32_t parit
 
 // What a CTA knows of its range.
 struct PagedSched {
-    int64_t T, t_begin, t_end;  // tiles of all items; this CTA's range
-    int64_t off_b;              // tile offset of request b
-    int b;                      // request of the range's first tile
+    int64_t T, t_begin, t_end;  // units of all items; this CTA's range
+    int64_t off_b;              // unit offset of request b
+    int b;                      // request of the range's first unit
     int grid;                   // CTAs with work
     int abort;
     int last;                   // this CTA arrived last at the item
+};
+
+// The parts of a split item: its tiles' owners are CTAs lo .. lo + n - 1 (a
+// range holds at least two units, so each owns one of its tiles). A CTA has a
+// slot for the item that begins at or before its range (0) and one for the
+// item that its end cuts (1).
+struct PagedParts {
+    int64_t lo;
+    int n;
+    int slot_lo;  // the first part's slot
+    __device__ __forceinline__ PagedParts(const PagedSched &w, int64_t off, int tiles, int us) {
+        lo = tile_owner(off, w.T, w.grid);
+        n = (int)(tile_owner(off + ((int64_t)(tiles - 1) << us), w.T, w.grid) - lo) + 1;
+        slot_lo = off > tile_begin(lo, w.T, w.grid) ? 1 : 0;
+    }
 };
 
 // A CTA's place in its range: one item (segment) after the other.
 struct PagedWalk {
     PagedSeq s;
     int b, kv, rb, local, tiles;  // tile `local` of the item's `tiles`
-    int64_t off, remaining;       // tile offset of the item
-    bool first;
-    __device__ __forceinline__ void init(const PagedWorkParams &p, const PagedSched &w) {
+    int us;                       // log2 of the units of its tiles
+    int64_t off, begin, end;      // unit offset of the item; the range
+    // False when the range holds no tile.
+    __device__ __forceinline__ bool init(const PagedWorkParams &p, const PagedSched &w) {
         b = w.b;
         s.load(p, b);
-        const int64_t head = head_tiles(s, p.tbs), rel = w.t_begin - w.off_b;
+        const int64_t head = head_units(s, p), rel = w.t_begin - w.off_b;
         kv = (int)(rel / head);
         const int64_t in_head = rel - kv * head;
         int lo = 0, hi = ((s.m - 1) >> p.tbs) + 1;  // the last block that begins at or before in_head
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (tiles_before(s, mid, p.tbs) <= in_head) lo = mid; else hi = mid;
+            if (units_before(s, mid, p) <= in_head) lo = mid; else hi = mid;
         }
         rb = lo;
-        const int64_t before = tiles_before(s, rb, p.tbs);
-        local = (int)(in_head - before);
+        us = unit_shift(s, rb, p);
+        const int64_t before = units_before(s, rb, p);
+        local = (int)((in_head - before + us) >> us);  // a tile begun in the last range is not this one's
         tiles = block_tiles(s, rb, p.tbs);
         off = w.off_b + kv * head + before;
-        remaining = w.t_end - w.t_begin;
-        first = true;
+        begin = w.t_begin;
+        end = w.t_end;
+        return local < tiles || advance(p);
     }
+    // Tiles of the item in this range, from `local` on.
     __device__ __forceinline__ int seg_len() const {
-        const int64_t r = tiles - local;
-        return (int)(r < remaining ? r : remaining);
+        const int64_t n = (end - off + us) >> us;
+        return (int)(n < tiles ? n : tiles) - local;
     }
-    __device__ __forceinline__ bool whole() const { return local == 0 && tiles <= remaining; }
-    // Move past a segment of n tiles; false when the range is done.
-    __device__ __forceinline__ bool next(int n, const PagedWorkParams &p) {
-        remaining -= n;
-        first = false;
-        if (remaining <= 0) return false;
-        off += tiles;
+    __device__ __forceinline__ bool whole() const { return local == 0 && seg_len() == tiles; }
+    // To the next item with a tile; false when the range is done.
+    __device__ __forceinline__ bool advance(const PagedWorkParams &p) {
+        off += (int64_t)tiles << us;
+        if (off >= end) return false;
         local = 0;
         do {
             if (((int64_t)(rb + 1) << p.tbs) < s.m) {
@@ -203,14 +234,16 @@ struct PagedWalk {
             }
             tiles = block_tiles(s, rb, p.tbs);
         } while (tiles == 0);
+        us = unit_shift(s, rb, p);
         return true;
     }
+    __device__ __forceinline__ int slot() const { return off > begin ? 1 : 0; }  // of its partial
 };
 
-// Threads 0 .. 255 (whole CTA must call; it has __syncthreads): the tiles of
-// all items, and the request that holds the range's first tile. scratch: 8
-// words of 64 bits. min_tiles: a small step keeps this many tiles per CTA.
-__device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSched *sched, int64_t *scratch, int min_tiles) {
+// Threads 0 .. 255 (whole CTA must call; it has __syncthreads): the units of
+// all items, and the request that holds the range's first unit. scratch: 8
+// words of 64 bits. min_units: every CTA with work has at least this many.
+__device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSched *sched, int64_t *scratch, int min_units) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + 255) / 256;
     int64_t mine = 0, incl = 0;
@@ -221,7 +254,7 @@ __device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSc
         for (int b = b0; b < b1; ++b) {
             PagedSeq s;
             s.load(p, b);
-            mine += p.Hkv * head_tiles(s, p.tbs);
+            mine += p.Hkv * head_units(s, p);
         }
         incl = mine;
 #pragma unroll
@@ -239,10 +272,10 @@ __device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSc
             if (w < warp) base += scratch[w];
             total += scratch[w];
         }
-        const int64_t want = (total + min_tiles - 1) / min_tiles;
-        const int grid = want < (int64_t)gridDim.x ? (int)want : (int)gridDim.x;
+        const int64_t most = total / min_units;
+        const int grid = most < (int64_t)gridDim.x ? (most > 0 ? (int)most : 1) : (int)gridDim.x;
         int64_t tb = 0, te = 0;
-        if ((int)blockIdx.x < grid) {
+        if (total > 0 && (int)blockIdx.x < grid) {
             tb = tile_begin(blockIdx.x, total, grid);
             te = tile_begin(blockIdx.x + 1, total, grid);
         }
@@ -255,11 +288,11 @@ __device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSc
             sched->abort = 0;
             sched->last = 0;
         }
-        if (tb < te && off <= tb && tb < off + mine) {  // one thread's requests hold tile tb
+        if (tb < te && off <= tb && tb < off + mine) {  // one thread's requests hold unit tb
             for (int b = b0; b < b1; ++b) {
                 PagedSeq s;
                 s.load(p, b);
-                const int64_t n = p.Hkv * head_tiles(s, p.tbs);
+                const int64_t n = p.Hkv * head_units(s, p);
                 if (tb < off + n) {
                     sched->b = b;
                     sched->off_b = off;
