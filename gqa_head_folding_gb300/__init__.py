@@ -716,11 +716,12 @@ def _paged_bad(name: str, t, dtype, shape, dev: int):
 
 def _paged(name: str, t, dtype, shape, dev: int) -> int:
     """Address of a contiguous tensor of this dtype and shape on the current device."""
-    if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
-        _paged_bad(name, t, dtype, shape, dev)
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _paged_bad(name, t, dtype, shape, dev)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _paged_bad(name, t, dtype, shape, dev)
 
 
 def _paged_dim(name: str, t, ndim: int):
@@ -784,7 +785,8 @@ def paged_build_tables(cache_len, new_len, free_pages, free_count, block_table, 
         _paged("cu_q", cu_q, i32, (B + 1,), dev), _paged("positions", positions, i32, per_t, dev),
         _paged("slots", slots, i32, per_t, dev), _paged("free_count_out", free_count_out, i32, one, dev),
         _cuda_stream(dev))
-    _check("paged_build_tables", status)
+    if status:
+        _check("paged_build_tables", status)
     return kv_len, cu_q, positions, slots, free_count_out
 
 
@@ -805,7 +807,8 @@ def paged_release_pages(kv_len, keep_len, block_table, free_pages, free_count, p
         _paged("block_table", block_table, i32, (B, width), dev), _paged("free_pages", free_pages, i32, (pool,), dev),
         _paged("free_count", free_count, i32, (1,), dev), _paged("free_count_out", free_count_out, i32, (1,), dev),
         _cuda_stream(dev))
-    _check("paged_release_pages", status)
+    if status:
+        _check("paged_release_pages", status)
     return free_count_out
 
 
@@ -851,7 +854,8 @@ def paged_norm_rope_append(q, k, v, positions, slots, k_pages, v_pages, q_weight
         1 if interleaved else 0, _paged("q_out", q_out, dt, (T, Hq, D), dev),
         _paged("k_pages", k_pages, dt, (num_pages, Hkv, S, D), dev), _paged("v_pages", v_pages, dt, pool, dev),
         _cuda_stream(dev))
-    _check("paged_norm_rope_append", status)
+    if status:
+        _check("paged_norm_rope_append", status)
     return q_out
 
 
@@ -882,5 +886,6 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, cu_q, kv_len, scale: float,
         _paged("block_table", block_table, i32, (B, max_pages), dev), _paged("cu_q", cu_q, i32, (B + 1,), dev),
         _paged("kv_len", kv_len, i32, (B,), dev), scale, _paged("out", out, dt, rows, dev),
         _paged("workspace", workspace, torch.uint8, (nbytes,), dev), nbytes, _cuda_stream(dev))
-    _check("gqa_paged_attn", status)
+    if status:
+        _check("gqa_paged_attn", status)
     return out

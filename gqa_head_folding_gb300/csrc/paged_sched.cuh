@@ -155,6 +155,19 @@ __device__ __forceinline__ bool warp_mbar_wait_slow(uint32_t bar, uint32_t parit
     }
 }
 
+// First unit of CTA c's range, and the CTA whose range holds unit t: in 32 bits
+// where they suffice (a 64-bit division is a long sequence, and these stand
+// between the launch and the first load).
+constexpr int64_t kSmallUnits = 1 << 22;
+__device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t T, int grid) {
+    if (T < kSmallUnits && grid < 1024) return (uint32_t)c * (uint32_t)T / (uint32_t)grid;
+    return tile_begin(c, T, grid);
+}
+__device__ __forceinline__ int64_t unit_owner(int64_t t, int64_t T, int grid) {
+    if (T < kSmallUnits && grid < 1024) return (((uint32_t)t + 1u) * (uint32_t)grid - 1u) / (uint32_t)T;
+    return tile_owner(t, T, grid);
+}
+
 // What a CTA knows of its range.
 struct PagedSched {
     int64_t T, t_begin, t_end;  // units of all items; this CTA's range
@@ -174,9 +187,9 @@ struct PagedParts {
     int n;
     int slot_lo;  // the first part's slot
     __device__ __forceinline__ PagedParts(const PagedSched &w, int64_t off, int tiles, int us) {
-        lo = tile_owner(off, w.T, w.grid);
-        n = (int)(tile_owner(off + ((int64_t)(tiles - 1) << us), w.T, w.grid) - lo) + 1;
-        slot_lo = off > tile_begin(lo, w.T, w.grid) ? 1 : 0;
+        lo = unit_owner(off, w.T, w.grid);
+        n = (int)(unit_owner(off + ((int64_t)(tiles - 1) << us), w.T, w.grid) - lo) + 1;
+        slot_lo = off > unit_begin(lo, w.T, w.grid) ? 1 : 0;
     }
 };
 
@@ -191,7 +204,7 @@ struct PagedWalk {
         b = w.b;
         s.load(p, b);
         const int64_t head = head_units(s, p), rel = w.t_begin - w.off_b;
-        kv = (int)(rel / head);
+        kv = w.T < kSmallUnits ? (int)((uint32_t)rel / (uint32_t)head) : (int)(rel / head);
         const int64_t in_head = rel - kv * head;
         int lo = 0, hi = ((s.m - 1) >> p.tbs) + 1;  // the last block that begins at or before in_head
         while (hi - lo > 1) {
@@ -272,12 +285,12 @@ __device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSc
             if (w < warp) base += scratch[w];
             total += scratch[w];
         }
-        const int64_t most = total / min_units;
+        const int64_t most = total < kSmallUnits ? (int64_t)((uint32_t)total / (uint32_t)min_units) : total / min_units;
         const int grid = most < (int64_t)gridDim.x ? (most > 0 ? (int)most : 1) : (int)gridDim.x;
         int64_t tb = 0, te = 0;
         if (total > 0 && (int)blockIdx.x < grid) {
-            tb = tile_begin(blockIdx.x, total, grid);
-            te = tile_begin(blockIdx.x + 1, total, grid);
+            tb = unit_begin(blockIdx.x, total, grid);
+            te = unit_begin(blockIdx.x + 1, total, grid);
         }
         int64_t off = base + incl - mine;
         if (tid == 0) {
@@ -290,9 +303,12 @@ __device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSc
         }
         if (tb < te && off <= tb && tb < off + mine) {  // one thread's requests hold unit tb
             for (int b = b0; b < b1; ++b) {
-                PagedSeq s;
-                s.load(p, b);
-                const int64_t n = p.Hkv * head_units(s, p);
+                int64_t n = mine;
+                if (per > 1) {
+                    PagedSeq s;
+                    s.load(p, b);
+                    n = p.Hkv * head_units(s, p);
+                }
                 if (tb < off + n) {
                     sched->b = b;
                     sched->off_b = off;
