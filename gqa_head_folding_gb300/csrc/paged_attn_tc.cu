@@ -55,6 +55,7 @@ struct PtcCfg {
 };
 
 constexpr int kMinUnits = 2;        // units per CTA below which a small step uses fewer CTAs (two at least: see PagedParts)
+constexpr int kItemUnits = 5;       // what an item costs beside its tiles: its start, epilogue and merge, in tiles of one row tile
 constexpr float kSumLimit = 32768.f;  // of 64 P: above it some P passes 2^9
 constexpr float kRefMove = 9.f;       // log2 of the P that moves a row's reference
 constexpr float kRefDrop = 6.f;       // the new reference's distance under the row's maximum
@@ -169,6 +170,21 @@ struct PtcSegment {
     int v_before;  // V tiles before this segment
     int more;
 };
+
+// One thread's work on it, as calls of their own: in registers, away from the
+// loop's (on the copy in shared memory the first took 2.9 us).
+__device__ __noinline__ bool segment_begin(PagedWalk &to, const PagedWorkParams &p, const PagedSched &sched) {
+    PagedWalk w;
+    const bool more = w.init(p, sched);
+    to = w;
+    return more;
+}
+__device__ __noinline__ bool segment_next(PagedWalk &at, const PagedWorkParams &p) {
+    PagedWalk w = at;
+    const bool more = w.advance(p);
+    at = w;
+    return more;
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
@@ -451,7 +467,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             uint32_t oph = 0;  // phase of o_done
             bool ok = true;
             if (tid == 0) {
-                seg_s->more = seg_s->w.init(p.w, *sched);
+                seg_s->more = segment_begin(seg_s->w, p.w, *sched);
                 seg_s->v_before = 0;
             }
             named_bar_sync(1, 512);
@@ -696,10 +712,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                     }
                     named_bar_sync(1, 512);
                     if (sched->last && live) {
-                        // partials: slot 0 (a range's first segment), but the first CTA's,
-                        // which is its last unless the item begins its range
                         const float *base = p.part + parts.lo * 2 * C::PART;
-                        auto part_of = [&](int i) { return base + (int64_t)(2 * i + (i == 0 ? parts.slot_lo : 0)) * C::PART; };
+                        auto part_of = [&](int i) { return base + (int64_t)(2 * i + (i == 0 ? 1 : 0)) * C::PART; };
                         float mx = -INFINITY, sum = 0.f;
                         for (int i = 0; i < np; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + 2 * rho));
                         for (int i = 0; i < np; ++i) {
@@ -742,7 +756,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 named_bar_sync(1, 512);  // the segment has been read
                 if (tid == 0) {
                     seg_s->v_before += n;
-                    seg_s->more = seg_s->w.advance(p.w);
+                    seg_s->more = segment_next(seg_s->w, p.w);
                 }
                 named_bar_sync(1, 512);
             }
@@ -771,7 +785,7 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     
     p.G = d.num_q_heads / d.num_kv_heads;
     p.gshift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3;
-    fill_paged_work(a, 8 - p.gshift, 128 >> p.gshift, p.w);  // blocks of 256 rows; above 128 a tile runs twice
+    fill_paged_work(a, 8 - p.gshift, 128 >> p.gshift, kItemUnits, p.w);  // blocks of 256 rows; above 128 a tile runs twice
     CUtensorMap qmap, kmap, vmap;
     if (!encode_tensor_map_heads(&qmap, a.q, d.max_tokens, d.num_q_heads, D, p.G, 128 / p.G)) return GQAQ_ERR_CUDA;
     if (!encode_tensor_map_2d(&kmap, a.k_pages, rows, D, 64, d.page_size, true)) return GQAQ_ERR_CUDA;

@@ -5,11 +5,13 @@
 // r / G, head r % G. An item's context is cut into tiles of 128 tokens, up to
 // its last row's position. A tile costs one unit, or two where the block has
 // more than `half` tokens (the tensor-memory kernel runs it for two row
-// tiles). The units of all items, in the order (request, KV head, block,
+// tiles), and an item `extra` units before its first tile, for what it costs
+// beside its tiles (a batch of 30 short contexts and two chunks ended between
+// 59 and 94 us without them). The units of all items, in the order (request, KV head, block,
 // tile), are split into equal contiguous ranges, one per CTA, so a batch of
 // unlike lengths loads all SMs alike; consecutive CTAs work on the same keys,
-// which the L2 then serves. A tile is its first unit's owner's. An item cut by
-// a range boundary is merged by the CTA that finishes last.
+// which the L2 then serves. A tile is its first unit's owner's. An item whose
+// tiles have several owners is merged by the one that finishes last.
 #pragma once
 
 #include "internal.h"
@@ -24,11 +26,12 @@ struct PagedWorkParams {
     int shift;             // log2 of the page size
     int tbs;               // log2 of TB, the tokens per block
     int half;              // tokens of a block above which its tiles cost two units
+    int extra;             // units of an item beside its tiles'
     int num_pages, max_pages;
     int64_t room;          // max_pages * page size
 };
 
-inline void fill_paged_work(const PagedAttnArgs &a, int tbs, int half, PagedWorkParams &w) {
+inline void fill_paged_work(const PagedAttnArgs &a, int tbs, int half, int extra, PagedWorkParams &w) {
     const gqaq_paged_dims &d = *a.dims;
     w.table = a.block_table;
     w.cu_q = a.cu_q;
@@ -39,6 +42,7 @@ inline void fill_paged_work(const PagedAttnArgs &a, int tbs, int half, PagedWork
     w.max_q = a.max_q_len;
     w.tbs = tbs;
     w.half = half;
+    w.extra = extra;
     w.shift = 0;
     while ((1 << w.shift) < d.page_size) ++w.shift;
     w.num_pages = d.num_pages;
@@ -106,12 +110,16 @@ __device__ __forceinline__ int unit_shift(const PagedSeq &s, int rb, const Paged
 // Units of the first rb blocks (each but a request's last is whole, hence of
 // one kind), and of all blocks of a head.
 __device__ __forceinline__ int64_t units_before(const PagedSeq &s, int rb, const PagedWorkParams &p) {
-    return tiles_before(s, rb, p.tbs) << unit_shift(s, 0, p);
+    const int empty = s.start < 0 ? min(rb, -s.start >> p.tbs) : 0;  // blocks that end before position zero
+    return (tiles_before(s, rb, p.tbs) << unit_shift(s, 0, p)) + (int64_t)p.extra * (rb - empty);
+}
+__device__ __forceinline__ int64_t item_units(int tiles, int us, const PagedWorkParams &p) {
+    return tiles > 0 ? ((int64_t)tiles << us) + p.extra : 0;
 }
 __device__ __forceinline__ int64_t head_units(const PagedSeq &s, const PagedWorkParams &p) {
     if (s.m <= 0) return 0;
     const int last = (s.m - 1) >> p.tbs;
-    return units_before(s, last, p) + ((int64_t)block_tiles(s, last, p.tbs) << unit_shift(s, last, p));
+    return units_before(s, last, p) + item_units(block_tiles(s, last, p.tbs), unit_shift(s, last, p), p);
 }
 
 // Up to 64 probes of a barrier's phase in the shortest loop there is: a
@@ -179,17 +187,17 @@ struct PagedSched {
 };
 
 // The parts of a split item: its tiles' owners are CTAs lo .. lo + n - 1 (a
-// range holds at least two units, so each owns one of its tiles). A CTA has a
-// slot for the item that begins at or before its range (0) and one for the
-// item that its end cuts (1).
+// range holds at least two units, so each owns one of its tiles). A CTA keeps
+// one partial without the item's first tile (slot 0: of the item its range
+// begins in) and one with it (slot 1: of the item its end cuts), so the first
+// part lies in slot 1 and the others in slot 0.
 struct PagedParts {
     int64_t lo;
     int n;
-    int slot_lo;  // the first part's slot
+    // off: unit of the item's first tile
     __device__ __forceinline__ PagedParts(const PagedSched &w, int64_t off, int tiles, int us) {
         lo = unit_owner(off, w.T, w.grid);
         n = (int)(unit_owner(off + ((int64_t)(tiles - 1) << us), w.T, w.grid) - lo) + 1;
-        slot_lo = off > unit_begin(lo, w.T, w.grid) ? 1 : 0;
     }
 };
 
@@ -198,7 +206,7 @@ struct PagedWalk {
     PagedSeq s;
     int b, kv, rb, local, tiles;  // tile `local` of the item's `tiles`
     int us;                       // log2 of the units of its tiles
-    int64_t off, begin, end;      // unit offset of the item; the range
+    int64_t off, end;             // unit of the item's first tile; end of the range
     // False when the range holds no tile.
     __device__ __forceinline__ bool init(const PagedWorkParams &p, const PagedSched &w) {
         b = w.b;
@@ -213,13 +221,13 @@ struct PagedWalk {
         }
         rb = lo;
         us = unit_shift(s, rb, p);
-        const int64_t before = units_before(s, rb, p);
-        local = (int)((in_head - before + us) >> us);  // a tile begun in the last range is not this one's
         tiles = block_tiles(s, rb, p.tbs);
-        off = w.off_b + kv * head + before;
-        begin = w.t_begin;
+        off = w.off_b + kv * head + units_before(s, rb, p) + p.extra;
         end = w.t_end;
-        return local < tiles || advance(p);
+        const int64_t past = w.t_begin - off;
+        local = past <= 0 ? 0 : (int)((past + us) >> us);  // a tile begun in the last range is not this one's
+        if (local >= tiles) return advance(p);
+        return seg_len() > 0;
     }
     // Tiles of the item in this range, from `local` on.
     __device__ __forceinline__ int seg_len() const {
@@ -227,9 +235,10 @@ struct PagedWalk {
         return (int)(n < tiles ? n : tiles) - local;
     }
     __device__ __forceinline__ bool whole() const { return local == 0 && seg_len() == tiles; }
-    // To the next item with a tile; false when the range is done.
+    __device__ __forceinline__ int slot() const { return local == 0 ? 1 : 0; }  // of its partial
+    // To the next item with a tile in the range; false when there is none.
     __device__ __forceinline__ bool advance(const PagedWorkParams &p) {
-        off += (int64_t)tiles << us;
+        off += ((int64_t)tiles << us) + p.extra;
         if (off >= end) return false;
         local = 0;
         do {
@@ -250,7 +259,6 @@ struct PagedWalk {
         us = unit_shift(s, rb, p);
         return true;
     }
-    __device__ __forceinline__ int slot() const { return off > begin ? 1 : 0; }  // of its partial
 };
 
 // Threads 0 .. 255 (whole CTA must call; it has __syncthreads): the units of
