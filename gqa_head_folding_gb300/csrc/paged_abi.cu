@@ -19,7 +19,8 @@ int check_paged(const gqaq_paged_dims *d, bool heads) {
     if (d->batch < 1 || d->page_size < 1 || d->num_pages < 1 || d->max_pages < 1 || d->max_tokens < 1)
         return GQAQ_ERR_INVALID_ARG;
     if (!page_size_ok(d->page_size) || d->batch > kMaxBatch || d->max_tokens > kMaxTokens) return GQAQ_ERR_UNSUPPORTED;
-    if ((int64_t)d->max_pages * d->page_size > INT32_MAX || (int64_t)d->num_pages * d->page_size > INT32_MAX ||
+    // positions, slots and their tiles' ends are 32-bit numbers
+    if ((int64_t)d->max_pages * d->page_size > INT32_MAX - 1024 || (int64_t)d->num_pages * d->page_size > INT32_MAX - 1024 ||
         (int64_t)d->batch * d->max_pages > INT32_MAX)
         return GQAQ_ERR_UNSUPPORTED;
     if (!heads) return GQAQ_OK;
@@ -66,6 +67,7 @@ int paged_release_pages(const gqaq_paged_dims *dims, const int32_t *kv_len, cons
     if (!aligned4(kv_len) || !aligned4(keep_len) || !aligned4(block_table) || !aligned4(free_pages) ||
         !aligned4(free_count) || !aligned4(free_count_out))
         return GQAQ_ERR_INVALID_ARG;
+    if (free_pages == block_table) return GQAQ_ERR_INVALID_ARG;  // read while it is written
     LaunchCtx ctx;
     rc = make_ctx(&ctx, stream);
     if (rc != GQAQ_OK) return rc;

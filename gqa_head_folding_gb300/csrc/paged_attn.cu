@@ -28,7 +28,7 @@ namespace gqaq {
 namespace {
 
 constexpr int kRows = 8;          // rows of an item: q_len * G at most
-constexpr int kItemUnits = 1;     // what an item costs beside its tiles, in tiles
+constexpr int kItemTiles = 1;     // what an item costs beside its tiles, in tiles
 constexpr int kMinUnits = 2;      // tiles per CTA below which a small step uses fewer CTAs (four: 11.0 us for 32 KV-head contexts of 4K, two: 9.9)
 
 template <int D>
@@ -456,7 +456,7 @@ int launch_decode(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (!encode_tensor_map_kpage(&vmap, a.v_pages, rows, D, d.page_size)) return GQAQ_ERR_CUDA;
     const int G = d.num_q_heads / d.num_kv_heads;
     PdParams p;
-    fill_paged_work(a, 23, 1 << 23, kItemUnits, p.w);  // one block: every token of a request
+    fill_paged_work(a, 23, 1 << 23, kItemTiles, p.w);  // one block: every token of a request
     p.q = static_cast<const uint16_t *>(a.q);
     p.out = static_cast<uint16_t *>(a.out);
     p.count = reinterpret_cast<unsigned *>(a.workspace);

@@ -55,7 +55,7 @@ struct PtcCfg {
 };
 
 constexpr int kMinUnits = 2;        // units per CTA below which a small step uses fewer CTAs (two at least: see PagedParts)
-constexpr int kItemUnits = 5;       // what an item costs beside its tiles: its start, epilogue and merge, in tiles of one row tile
+constexpr int kItemTiles = 5;       // what an item costs beside its tiles: its start, epilogue and merge, in tiles (without it a mixed batch took 95 us for 74)
 constexpr float kSumLimit = 32768.f;  // of 64 P: above it some P passes 2^9
 constexpr float kRefMove = 9.f;       // log2 of the P that moves a row's reference
 constexpr float kRefDrop = 6.f;       // the new reference's distance under the row's maximum
@@ -785,7 +785,7 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     
     p.G = d.num_q_heads / d.num_kv_heads;
     p.gshift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3;
-    fill_paged_work(a, 8 - p.gshift, 128 >> p.gshift, kItemUnits, p.w);  // blocks of 256 rows; above 128 a tile runs twice
+    fill_paged_work(a, 8 - p.gshift, 128 >> p.gshift, kItemTiles, p.w);  // blocks of 256 rows; above 128 a tile runs twice
     CUtensorMap qmap, kmap, vmap;
     if (!encode_tensor_map_heads(&qmap, a.q, d.max_tokens, d.num_q_heads, D, p.G, 128 / p.G)) return GQAQ_ERR_CUDA;
     if (!encode_tensor_map_2d(&kmap, a.k_pages, rows, D, 64, d.page_size, true)) return GQAQ_ERR_CUDA;

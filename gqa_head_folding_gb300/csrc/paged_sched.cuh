@@ -5,8 +5,8 @@
 // r / G, head r % G. An item's context is cut into tiles of 128 tokens, up to
 // its last row's position. A tile costs one unit, or two where the block has
 // more than `half` tokens (the tensor-memory kernel runs it for two row
-// tiles), and an item `extra` units before its first tile, for what it costs
-// beside its tiles (a batch of 30 short contexts and two chunks ended between
+// tiles), and an item costs as `extra` more tiles before its first, for what
+// it takes beside its tiles (a batch of 30 short contexts and two chunks ended between
 // 59 and 94 us without them). The units of all items, in the order (request, KV head, block,
 // tile), are split into equal contiguous ranges, one per CTA, so a batch of
 // unlike lengths loads all SMs alike; consecutive CTAs work on the same keys,
@@ -26,7 +26,7 @@ struct PagedWorkParams {
     int shift;             // log2 of the page size
     int tbs;               // log2 of TB, the tokens per block
     int half;              // tokens of a block above which its tiles cost two units
-    int extra;             // units of an item beside its tiles'
+    int extra;             // what an item costs beside its tiles, in tiles
     int num_pages, max_pages;
     int64_t room;          // max_pages * page size
 };
@@ -111,10 +111,10 @@ __device__ __forceinline__ int unit_shift(const PagedSeq &s, int rb, const Paged
 // one kind), and of all blocks of a head.
 __device__ __forceinline__ int64_t units_before(const PagedSeq &s, int rb, const PagedWorkParams &p) {
     const int empty = s.start < 0 ? min(rb, -s.start >> p.tbs) : 0;  // blocks that end before position zero
-    return (tiles_before(s, rb, p.tbs) << unit_shift(s, 0, p)) + (int64_t)p.extra * (rb - empty);
+    return (tiles_before(s, rb, p.tbs) + (int64_t)p.extra * (rb - empty)) << unit_shift(s, 0, p);
 }
 __device__ __forceinline__ int64_t item_units(int tiles, int us, const PagedWorkParams &p) {
-    return tiles > 0 ? ((int64_t)tiles << us) + p.extra : 0;
+    return tiles > 0 ? (int64_t)(tiles + p.extra) << us : 0;
 }
 __device__ __forceinline__ int64_t head_units(const PagedSeq &s, const PagedWorkParams &p) {
     if (s.m <= 0) return 0;
@@ -222,7 +222,7 @@ struct PagedWalk {
         rb = lo;
         us = unit_shift(s, rb, p);
         tiles = block_tiles(s, rb, p.tbs);
-        off = w.off_b + kv * head + units_before(s, rb, p) + p.extra;
+        off = w.off_b + kv * head + units_before(s, rb, p) + (p.extra << us);
         end = w.t_end;
         const int64_t past = w.t_begin - off;
         local = past <= 0 ? 0 : (int)((past + us) >> us);  // a tile begun in the last range is not this one's
@@ -238,8 +238,7 @@ struct PagedWalk {
     __device__ __forceinline__ int slot() const { return local == 0 ? 1 : 0; }  // of its partial
     // To the next item with a tile in the range; false when there is none.
     __device__ __forceinline__ bool advance(const PagedWorkParams &p) {
-        off += ((int64_t)tiles << us) + p.extra;
-        if (off >= end) return false;
+        off += (int64_t)tiles << us;
         local = 0;
         do {
             if (((int64_t)(rb + 1) << p.tbs) < s.m) {
@@ -257,7 +256,8 @@ struct PagedWalk {
             tiles = block_tiles(s, rb, p.tbs);
         } while (tiles == 0);
         us = unit_shift(s, rb, p);
-        return true;
+        off += p.extra << us;
+        return off < end;
     }
 };
 

@@ -372,7 +372,8 @@ GQAQ_API int gqa_prefill_attn(const gqaq_dims *dims, int q_len, const gqaq_half 
  * q, k, v, out and the pages are fp16 or bfloat16 (dims.dtype, passed as
  * gqaq_half bits). Supported: D in {64, 128}; G in {1, 2, 4, 8}; S in
  * {8, 16, 32, 64, 128}; B <= 8192; max_tokens <= 2^22; max_pages * S,
- * B * max_pages and num_pages * Hkv * S below 2^31. Else GQAQ_ERR_UNSUPPORTED.
+ * B * max_pages and num_pages * Hkv * S below 2^31 - 1024; max_tokens * Hq
+ * below 2^30. Else GQAQ_ERR_UNSUPPORTED.
  *
  * As for every call, what lies on the device is checked there: lengths,
  * positions, slots and page indices out of range are clamped or skipped and
@@ -425,7 +426,8 @@ GQAQ_API int paged_build_tables(const gqaq_paged_dims *dims, const int32_t *cach
  * its pages from ceil(keep_len / S) to ceil(kv_len / S) are appended to
  * free_pages behind the first *free_count entries, in order of (request,
  * page). block_table is not changed: its entries past the kept length are no
- * longer the request's. free_count_out [1] (may be free_count itself) becomes
+ * longer the request's. A page that two rows share goes to the list once for
+ * each row that releases it: release shared pages with one row only. free_count_out [1] (may be free_count itself) becomes
  * the new count. A request with keep_len outside [0, kv_len] or kv_len
  * outside [0, max_pages * S] keeps all its pages and raises
  * GQAQ_DEV_BAD_LEN; pages that would pass the end of free_pages are dropped
@@ -480,7 +482,7 @@ GQAQ_API size_t gqaq_paged_workspace_bytes(const gqaq_paged_dims *dims);
  * Rows outside [cu_q[0], cu_q[B]) of out are left as they were. Stale rows of
  * a page past kv_len may hold anything, NaN included; the values (v) of the
  * request's own tokens must be finite, or a token may see those of a later
- * token of its chunk.
+ * token of its chunk. Requests may share pages (a common prefix).
  * max_q_len: the host's bound on q_len (it selects the kernel). A request
  * with more raises GQAQ_DEV_BAD_LEN and only its first max_q_len tokens are
  * computed. kv_len outside [0, max_pages * S] is clamped and raises

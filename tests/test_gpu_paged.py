@@ -354,6 +354,23 @@ def test_attn_long_context_and_wide_offsets():
     assert torch.equal(kp[-1, :, 5], k[0]) and torch.equal(vp[-1, :, 5], k[0])
 
 
+@pytest.mark.parametrize("B, n", [(1500, 1), (300, 5), (700, 2)])
+def test_attn_many_requests(B, n):
+    rng = np.random.default_rng(B)
+    kv = [int(x) for x in rng.integers(n, 60, B)]
+    kv[7], kv[B - 1] = 1500, 700
+    attn_case([n] * B, kv, 4, 1, 64, 8, "f16", seed=B)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [40, 9, 1]])
+def test_attn_requests_share_pages(q_lens):
+    """A common prefix of ten pages: the three tables begin with the same entries."""
+    def mess(q, kp, vp, table, cu, kv):
+        table[1:, :10] = table[0, :10]
+        return q, kp, vp, table, cu, kv
+    attn_case(q_lens, [300, 170, 261], 4, 2, 128, 16, "bf16", seed=21, mess=mess)
+
+
 def test_attn_workspace_is_reused_and_left_zero():
     d = g.make_paged_dims(1, 8, 2, 128, 16, 1, 1, 1)
     ws = g.alloc_paged_workspace(d, DEV)

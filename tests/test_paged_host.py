@@ -54,9 +54,10 @@ def test_table_calls_refuse_pointers(L):
         assert tables(L, dims(), i, ODD) == g.GQAQ_ERR_INVALID_ARG
     assert tables(L, dims(), 5, FAKE) == g.GQAQ_ERR_INVALID_ARG  # kv_len in the place of cache_len
     for i in range(6):
-        p = [FAKE] * 6
+        p = [FAKE, FAKE, FAKE, OTHER, FAKE, FAKE]
         p[i] = None
         assert L.paged_release_pages(ctypes.byref(dims()), *p, None) == g.GQAQ_ERR_INVALID_ARG
+    assert L.paged_release_pages(ctypes.byref(dims()), *[FAKE] * 6, None) == g.GQAQ_ERR_INVALID_ARG  # the table as the list
 
 
 def append(L, d, q=FAKE, sq=2048, k=FAKE, sk=512, v=FAKE, sv=512, pos=FAKE, slots=FAKE, wq=None, wk=None, eps=1e-6, cs=FAKE, rope=64,
