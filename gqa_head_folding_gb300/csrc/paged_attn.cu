@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
     uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(merge) + C::MERGE);
     uint64_t *empty = full + C::NSTAGE;
     int64_t *scratch = reinterpret_cast<int64_t *>(empty + C::NSTAGE);
-    PagedSched *sched = reinterpret_cast<PagedSched *>(scratch + 8);
+    PagedSched *sched = reinterpret_cast<PagedSched *>(scratch + 12);
     PdSplit *split = reinterpret_cast<PdSplit *>(sched + 1);
-    static_assert((2 * C::NSTAGE + 8) * 8 + sizeof(PagedSched) + 2 * sizeof(PdSplit) <= C::MISC, "misc region");
+    static_assert((2 * C::NSTAGE + 12) * 8 + sizeof(PagedSched) + 2 * sizeof(PdSplit) <= C::MISC, "misc region");
     volatile int *abort_flag = &sched->abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
         prefetch_tensormap(&vmap);
     }
     pdl_wait_and_release();
-    paged_schedule(p.w, sched, scratch, kMinUnits);
+    paged_schedule(p.w, sched, scratch, kMinUnits, 0);
     if (warp < 8) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 256);
     if (sched->t_begin >= sched->t_end) return;
     PagedWalk w;

@@ -71,6 +71,7 @@ struct PtcParams {
     float scale_log2;
     uint64_t timeout_ns;
     int test_stall;
+    int wide_out;      // out is 32-byte aligned
 };
 
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
@@ -166,6 +167,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // loop over tiles, whose reloads missed the small L1 that is left beside the
 // tiles (2 of 3.5 thousand cycles per tile).
 struct PtcSegment {
+    PagedWorkParams p;  // the launch's, for the calls below (through a reference to the kernel's parameter each field was a slow load)
     PagedWalk w;
     int v_before;  // V tiles before this segment
     int more;
@@ -173,16 +175,19 @@ struct PtcSegment {
 
 // One thread's work on it, as calls of their own: in registers, away from the
 // loop's (on the copy in shared memory the first took 2.9 us).
-__device__ __noinline__ bool segment_begin(PagedWalk &to, const PagedWorkParams &p, const PagedSched &sched) {
+__device__ __noinline__ bool segment_begin(PtcSegment &at, const PagedSched &sched) {
+    const PagedWorkParams p = at.p;
+    const PagedSched s = sched;
     PagedWalk w;
-    const bool more = w.init(p, sched);
-    to = w;
+    const bool more = w.init(p, s);
+    at.w = w;
     return more;
 }
-__device__ __noinline__ bool segment_next(PagedWalk &at, const PagedWorkParams &p) {
-    PagedWalk w = at;
+__device__ __noinline__ bool segment_next(PtcSegment &at) {
+    const PagedWorkParams p = at.p;
+    PagedWalk w = at.w;
     const bool more = w.advance(p);
-    at = w;
+    at.w = w;
     return more;
 }
 
@@ -209,14 +214,15 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     uint64_t *o_done = p_ready + 2;   // [2]: a group's last PV of a segment
     uint64_t *o_free = o_done + 2;    // the epilogue has read O
     uint64_t *drain = o_free + 1;
-    int64_t *scratch = reinterpret_cast<int64_t *>(drain + 1);  // [8]
-    PagedSched *sched = reinterpret_cast<PagedSched *>(scratch + 8);
+    int64_t *scratch = reinterpret_cast<int64_t *>(drain + 1);  // [12]
+    PagedSched *sched = reinterpret_cast<PagedSched *>(scratch + 12);
     PtcSegment *seg_s = reinterpret_cast<PtcSegment *>(sched + 1);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(seg_s + 1);
-    static_assert(256 * 4 + (2 * C::NK + 2 * C::NV + 10 + 8) * 8 + sizeof(PagedSched) + sizeof(PtcSegment) + 8 <= C::MISC, "misc region");
+    static_assert(256 * 4 + (2 * C::NK + 2 * C::NV + 10 + 12) * 8 + sizeof(PagedSched) + sizeof(PtcSegment) + 8 <= C::MISC, "misc region");
     volatile int *abort_flag = &sched->abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) seg_s->p = p.w;
     if (warp == 16 && lane == 0) {
         for (int s = 0; s < C::NK; ++s) {
             mbar_init(smem_u32(&kfull[s]), 1);
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
     }
     pdl_wait_and_release();
     tc_fence_before();
-    paged_schedule(p.w, sched, scratch, kMinUnits);
+    paged_schedule(p.w, sched, scratch, kMinUnits, D / 64);  // a part of 256 rows is 66 KB per 64 channels: two units' time
     tc_fence_after();
     const uint32_t tbase = *tslot;
     if (warp < 16) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 512);
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             uint32_t oph = 0;  // phase of o_done
             bool ok = true;
             if (tid == 0) {
-                seg_s->more = segment_begin(seg_s->w, p.w, *sched);
+                seg_s->more = segment_begin(*seg_s, *sched);
                 seg_s->v_before = 0;
             }
             named_bar_sync(1, 512);
@@ -675,14 +681,16 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         }
                         if (!live) continue;
                         if (whole) {
+                            uint32_t x[8];
 #pragma unroll
-                            for (int e = 0; e < 16; e += 8) {
-                                uint4 x;
-                                x.x = pack2<BF16>(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-                                x.y = pack2<BF16>(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
-                                x.z = pack2<BF16>(__uint_as_float(a[e + 4]), __uint_as_float(a[e + 5]));
-                                x.w = pack2<BF16>(__uint_as_float(a[e + 6]), __uint_as_float(a[e + 7]));
-                                *reinterpret_cast<uint4 *>(dst + c + e) = x;
+                            for (int e = 0; e < 8; ++e) x[e] = pack2<BF16>(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+                            if (p.wide_out) {  // a lane's 32 bytes are one sector: half the stores of scattered rows
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(dst + c)),
+                                             "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                                             : "memory");
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
                             }
                         } else {
                             float4 *acc = reinterpret_cast<float4 *>(part + C::ML) + (int64_t)(c / 4) * C::RB + rho;
@@ -756,7 +764,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 named_bar_sync(1, 512);  // the segment has been read
                 if (tid == 0) {
                     seg_s->v_before += n;
-                    seg_s->more = segment_next(seg_s->w, p.w);
+                    seg_s->more = segment_next(*seg_s);
                 }
                 named_bar_sync(1, 512);
             }
@@ -801,6 +809,7 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (p.scale_log2 == 0.f) p.scale_log2 = 1e-30f;  // 2^(s - max) is 1 all the same, and a masked score's product stays -inf
     p.timeout_ns = ctx.timeout_ns;
     p.test_stall = ctx.test_stall;
+    p.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     const cudaError_t e = launch_kernel(paged_tc_kernel<D, BF16>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, ctx, 0, qmap,
                                         kmap, vmap, p);
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;

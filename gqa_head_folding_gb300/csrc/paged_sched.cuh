@@ -262,20 +262,38 @@ struct PagedWalk {
 };
 
 // Threads 0 .. 255 (whole CTA must call; it has __syncthreads): the units of
-// all items, and the request that holds the range's first unit. scratch: 8
+// all items, and the request that holds the range's first unit. scratch: 12
 // words of 64 bits. min_units: every CTA with work has at least this many.
-__device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSched *sched, int64_t *scratch, int min_units) {
+// merge > 0: few long items are not cut into the smallest parts. n parts of u
+// units each take u units' time, then n times a partial's reading by the CTA
+// that merges them, so of an item of U units the best u is near the root of U
+// times a part's cost in units (256 rows: 2 merge, 128 rows: 3/4 merge). A
+// 104-token chunk of a 7K context on one KV head took 61 us in parts of one tile.
+__device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSched *sched, int64_t *scratch, int min_units,
+                                               int merge) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + 255) / 256;
     int64_t mine = 0, incl = 0;
     int b0 = 0, b1 = 0;
+    int *longest_s = reinterpret_cast<int *>(scratch + 8);
     if (tid < 256) {
+        int longest = 0;  // of a request's items: units times four times a part's cost, over merge
         b0 = min(tid * per, p.B);
         b1 = min(b0 + per, p.B);
         for (int b = b0; b < b1; ++b) {
             PagedSeq s;
             s.load(p, b);
             mine += p.Hkv * head_units(s, p);
+            if (merge > 0 && s.m > 0) {
+                for (int rb = (s.m - 1) >> p.tbs, k = 0; rb >= 0 && k < 2; --rb, ++k) {  // the last block, and the last whole one
+                    const int us = unit_shift(s, rb, p);
+                    longest = max(longest, (int)min(item_units(block_tiles(s, rb, p.tbs), us, p), (int64_t)(1 << 24)) * (us ? 8 : 3));
+                }
+            }
+        }
+        if (merge > 0) {
+            longest = (int)__reduce_max_sync(0xffffffffu, (unsigned)longest);
+            if (lane == 0) longest_s[warp] = longest;
         }
         incl = mine;
 #pragma unroll
@@ -292,6 +310,12 @@ __device__ __forceinline__ void paged_schedule(const PagedWorkParams &p, PagedSc
         for (int w = 0; w < 8; ++w) {
             if (w < warp) base += scratch[w];
             total += scratch[w];
+        }
+        if (merge > 0) {
+            int longest = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) longest = max(longest, longest_s[w]);
+            min_units = max(min_units, (int)sqrtf((float)longest * (float)merge * 0.25f));
         }
         const int64_t most = total < kSmallUnits ? (int64_t)((uint32_t)total / (uint32_t)min_units) : total / min_units;
         const int grid = most < (int64_t)gridDim.x ? (most > 0 ? (int)most : 1) : (int)gridDim.x;
