@@ -19,6 +19,11 @@
 // segment the eight warps' states merge in shared memory; an item cut by a
 // range boundary leaves an fp32 partial and the CTA that arrives last merges
 // them.
+//
+// What bounds it: HBM (batch 8 at up to 64K, 8 KV heads of 128 channels: 222 us,
+// 6.66 TB/s, 98% of the copy rate); with little data the chain of schedule (2
+// us), first tile (1.3), tiles, state merge (0.6), arrival (1.1) and merge of
+// the parts (one request at 4K: 10.3 us).
 #include <math.h>
 
 #include "attn_mma.cuh"
@@ -488,6 +493,8 @@ size_t paged_attn_workspace_bytes(const gqaq_paged_dims *d, const LaunchCtx &ctx
 
 int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (a.workspace_bytes < paged_attn_workspace_bytes(a.dims, ctx)) return GQAQ_ERR_WORKSPACE;
+    // Up to eight rows per KV head: the decode kernel (one request at 4K 12.8 us against 20.9, batch 32 at D = 64 32.5
+    // against 49); above, the tensor-memory kernel (12 to 24 rows: 47 to 65 us against 52 to 196 with more N blocks).
     if ((int64_t)a.max_q_len * (a.dims->num_q_heads / a.dims->num_kv_heads) > kRows) return launch_paged_tc(a, ctx);
     if (a.dims->dtype == GQAQ_BF16) return a.dims->head_dim == 128 ? launch_decode<128, true>(a, ctx) : launch_decode<64, true>(a, ctx);
     return a.dims->head_dim == 128 ? launch_decode<128, false>(a, ctx) : launch_decode<64, false>(a, ctx);
