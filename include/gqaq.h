@@ -482,7 +482,8 @@ GQAQ_API size_t gqaq_paged_workspace_bytes(const gqaq_paged_dims *dims);
  * Rows outside [cu_q[0], cu_q[B]) of out are left as they were. Stale rows of
  * a page past kv_len may hold anything, NaN included; the values (v) of the
  * request's own tokens must be finite, or a token may see those of a later
- * token of its chunk. Requests may share pages (a common prefix).
+ * token of its chunk. Requests may share pages (a common prefix). out may be
+ * q itself; it must not overlap the other inputs.
  * max_q_len: the host's bound on q_len (it selects the kernel). A request
  * with more raises GQAQ_DEV_BAD_LEN and only its first max_q_len tokens are
  * computed. kv_len outside [0, max_pages * S] is clamped and raises

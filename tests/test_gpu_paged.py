@@ -354,7 +354,7 @@ def test_attn_long_context_and_wide_offsets():
     assert torch.equal(kp[-1, :, 5], k[0]) and torch.equal(vp[-1, :, 5], k[0])
 
 
-@pytest.mark.parametrize("B, n", [(1500, 1), (300, 5), (700, 2)])
+@pytest.mark.parametrize("B, n", [(1500, 1), (300, 5), (700, 2), (8192, 1)])
 def test_attn_many_requests(B, n):
     rng = np.random.default_rng(B)
     kv = [int(x) for x in rng.integers(n, 60, B)]
@@ -369,6 +369,35 @@ def test_attn_requests_share_pages(q_lens):
         table[1:, :10] = table[0, :10]
         return q, kp, vp, table, cu, kv
     attn_case(q_lens, [300, 170, 261], 4, 2, 128, 16, "bf16", seed=21, mess=mess)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [300, 2], [40, 150]])
+@pytest.mark.parametrize("pdl", [0, 1])
+def test_attn_output_in_place_of_q(q_lens, pdl):
+    g.set_option(g.GQAQ_OPT_PDL, pdl)
+    try:
+        q, kp, vp, table, cu, kv = paged_inputs(q_lens, [1200, 700], 8, 2, 64, 16, torch.float16, 30, DEV)
+        ref, tol = ref_attn(q, kp, vp, table, cu.tolist(), kv.tolist(), 0.125, torch.zeros_like(q))
+        assert g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.125, max(q_lens), out=q) is q
+        torch.cuda.synchronize()
+        assert ((q.double() - ref).abs() <= tol).all() and g.device_status() == 0
+    finally:
+        g.set_option(g.GQAQ_OPT_PDL, 1)
+
+
+def test_attn_a_bound_far_above_the_rows():
+    attn_case([1, 1, 1], [300, 1, 77], 2, 2, 64, 16, "f16", seed=31, max_q=2 ** 31 - 1)
+
+
+def test_attn_output_at_16_bytes():
+    """An out that is 16-byte but not 32-byte aligned."""
+    q, kp, vp, table, cu, kv = paged_inputs([200, 3], [400, 90], 4, 2, 128, 16, torch.bfloat16, 32, DEV)
+    room = torch.zeros(q.numel() + 8, dtype=q.dtype, device=DEV)
+    out = room[8:].view(q.shape)
+    ref, tol = ref_attn(q, kp, vp, table, cu.tolist(), kv.tolist(), 0.09, torch.zeros_like(q))
+    g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.09, 200, out=out)
+    torch.cuda.synchronize()
+    assert out.data_ptr() % 32 == 16 and ((out.double() - ref).abs() <= tol).all() and int(room[:8].count_nonzero()) == 0
 
 
 def test_attn_workspace_is_reused_and_left_zero():
