@@ -74,7 +74,10 @@ class PagedCache:
         torch.maximum(self.cache_len, self.kv_len, out=self.cache_len)
 
     def release(self, keep_len: torch.Tensor):
-        """Requests keep their first keep_len [batch] tokens; the pages past them are free again."""
+        """Requests keep their first keep_len [batch] tokens; the pages past them are free again. A request whose
+        keep_len is negative or above its length keeps its length and all its pages (GQAQ_DEV_BAD_LEN)."""
         paged_release_pages(self.cache_len, keep_len, self.block_table, self.free_pages, self.free_count, self.page_size,
                             free_count_out=self.free_count)
-        self.cache_len.copy_(keep_len)
+        # the lengths follow the library's rule, so that they never pass the tokens that the pages hold
+        kept = (keep_len >= 0) & (keep_len <= self.cache_len)
+        torch.where(kept, keep_len, self.cache_len, out=self.cache_len)
