@@ -8,9 +8,10 @@ Requests of unlike lengths share one pool of pages per layer. A step runs
   commit                            the lengths after the step
   release   paged_release_pages     pages of requests that ended, or of a rejected tail of drafted tokens
 
-with one plan for all layers: every layer's pools use the same page indices. Everything a step reads
-or writes on the device lies in buffers that this object keeps, so plan, append, attend and commit can
-be captured in a CUDA graph (after one eager step) and replayed with new contents of new_len.
+with one plan for all layers: every layer's pools use the same page indices. A planned step is
+committed or released before the next is planned (its pages are otherwise lost to the pool). Everything
+a step reads or writes on the device lies in buffers that this object keeps, so plan, append, attend and
+commit can be captured in a CUDA graph (after one eager step) and replayed with new contents of new_len.
 
 This module only sequences library calls and owns the buffers they share.
 """
@@ -74,10 +75,13 @@ class PagedCache:
         torch.maximum(self.cache_len, self.kv_len, out=self.cache_len)
 
     def release(self, keep_len: torch.Tensor):
-        """Requests keep their first keep_len [batch] tokens; the pages past them are free again. A request whose
-        keep_len is negative or above its length keeps its length and all its pages (GQAQ_DEV_BAD_LEN)."""
-        paged_release_pages(self.cache_len, keep_len, self.block_table, self.free_pages, self.free_count, self.page_size,
+        """Requests keep their first keep_len [batch] tokens; the pages past them are free again. Before commit the
+        planned step counts, so keep_len can give it up, or keep part of it. A request whose keep_len is negative or
+        above its length keeps its lengths and all its pages (GQAQ_DEV_BAD_LEN)."""
+        held = torch.maximum(self.cache_len, self.kv_len)  # with a planned step that commit has not seen
+        paged_release_pages(held, keep_len, self.block_table, self.free_pages, self.free_count, self.page_size,
                             free_count_out=self.free_count)
-        # the lengths follow the library's rule, so that they never pass the tokens that the pages hold
-        kept = (keep_len >= 0) & (keep_len <= self.cache_len)
+        # both lengths follow the library's rule, so that neither they nor a later commit pass the tokens that the pages hold
+        kept = (keep_len >= 0) & (keep_len <= held)
         torch.where(kept, keep_len, self.cache_len, out=self.cache_len)
+        torch.where(kept, keep_len, self.kv_len, out=self.kv_len)

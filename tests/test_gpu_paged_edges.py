@@ -64,3 +64,36 @@ def test_release_of_a_request_that_the_plan_refused():
     release_some(L, [0, 40])
     L.step([0, 20])
     assert g.device_status() == 0 and L.len.tolist() == [0, 60]
+
+
+def test_commit_after_a_release_brings_nothing_back():
+    L = Loop(3, 4, 2, 64, 16, torch.float16, 24, 160, 120, seed=3)
+    L.step([40, 20, 33])
+    release_some(L, [0, 20, 17])
+    L.c.commit()
+    assert L.c.cache_len.tolist() == [0, 20, 17]
+    L.step([35, 5, 5])
+    assert g.device_status() == 0 and L.len.tolist() == [35, 25, 22]
+
+
+def test_release_of_a_planned_step():
+    """Before commit, release counts from the planned lengths: a step can be given up, or kept in part, and its pages go back."""
+    L = Loop(3, 4, 2, 64, 16, torch.float16, 24, 160, 120, seed=4)
+    L.step([40, 20, 33])
+    count = L.count
+    for keep in ([40, 20, 33], [45, 20, 60], [40, 20, 33]):
+        new = [20, 0, 40] if L.len[2] == 33 else [0, 0, 0]
+        kv = L.model_plan(new)[0]
+        L.c.plan(ints(new))
+        assert L.c.kv_len.tolist() == kv.tolist()
+        L.len = kv
+        release_some(L, keep)
+        L.c.commit()
+        assert L.c.cache_len.tolist() == keep
+    assert L.count == count
+    L.model_plan([20, 0, 40])
+    L.c.plan(ints([20, 0, 40]))
+    L.c.release(ints([61, 20, 33]))  # one too many: refused, its step stays planned; the other's is given up
+    assert g.device_status() == g.GQAQ_DEV_BAD_LEN
+    L.c.commit()
+    assert L.c.cache_len.tolist() == [60, 20, 33]
