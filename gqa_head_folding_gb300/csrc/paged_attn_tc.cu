@@ -735,7 +735,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         for (int i = 0; i < np; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + 2 * rho));
                         for (int i = 0; i < np; ++i) {
                             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(i)) + rho);
-                            if (ml.x != -INFINITY) sum += fast_exp2(ml.x - mx) * ml.y;
+                            // without a reference the sum is 0, or NaN where every score that the row sees in the part is
+                            sum += ml.x == -INFINITY ? ml.y : fast_exp2(ml.x - mx) * ml.y;
                         }
                         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll 1
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                             for (int i = 0; i < np; ++i) {
                                 const float *pi = part_of(i);
                                 const float m = __ldcg(pi + 2 * rho);
-                                const float f = m == -INFINITY ? 0.f : fast_exp2(m - mx) * inv;
+                                const float f = (m == -INFINITY ? 0.f : fast_exp2(m - mx)) * inv;  // NaN where inv is
                                 const float4 *acc = reinterpret_cast<const float4 *>(pi + C::ML) + (int64_t)(c / 4) * C::RB + rho;
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {

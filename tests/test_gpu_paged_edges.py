@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gqa_head_folding_gb300 as g
-from _paged import ref_release
+from _paged import DTYPES, pages_of, paged_inputs, ref_attn, ref_release
 from test_gpu_paged_run import Loop
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +97,55 @@ def test_release_of_a_planned_step():
     assert g.device_status() == g.GQAQ_DEV_BAD_LEN
     L.c.commit()
     assert L.c.cache_len.tolist() == [60, 20, 33]
+
+
+# ---------------------------------------------------------------------------
+# NaN and infinity in live rows
+# ---------------------------------------------------------------------------
+def softmax_rows(q, kp, vp, table, cu, kv, scale):
+    """The definition row by row in 64 bits, NaN and infinity included."""
+    out = torch.zeros_like(q, dtype=torch.float64)
+    S, G = kp.shape[2], q.shape[1] // kp.shape[1]
+    for b in range(len(kv)):
+        n, L = cu[b + 1] - cu[b], kv[b]
+        pg = table[b, :pages_of(L, S)].long()
+        k, v = (x[pg].double().transpose(1, 2).reshape(-1, x.shape[1], x.shape[3])[:L] for x in (kp, vp))
+        for i in range(n):
+            seen = L - n + i + 1
+            for h in range(q.shape[1]):
+                s = k[:seen, h // G] @ q[cu[b] + i, h].double() * scale
+                out[cu[b] + i, h] = torch.softmax(s, 0) @ v[:seen, h // G]
+    return out
+
+
+@pytest.mark.parametrize("what", ["a row of q", "a channel of q", "many keys", "an infinite key"])
+@pytest.mark.parametrize("ctas", [0, 5])
+@pytest.mark.parametrize("q_lens, kv_lens, G, D", [([1], [5000], 4, 128), ([1, 2], [300, 5000], 2, 64), ([40], [6000], 1, 128),
+                                                   ([40, 9], [100, 3100], 2, 64), ([200], [6000], 1, 64), ([150, 1], [150, 900], 2, 128)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attn_nan_and_infinity_reach_the_rows_that_see_them(dtype, q_lens, kv_lens, G, D, ctas, what):
+    """Whether one CTA holds an item or many share it, a row whose scores hold NaN (or +inf) is NaN, and no other is touched."""
+    g.set_option(g.GQAQ_OPT_MAX_CTAS, ctas)
+    q, kp, vp, table, cu, kv = paged_inputs(q_lens, kv_lens, G, 1, D, 16, DTYPES[dtype], 11, DEV)
+    scale = D ** -0.5
+    last = len(q_lens) - 1
+    row = int(cu[last]) + q_lens[last] // 2
+    q[row, 0, 9] = 1.0
+    _, tol = ref_attn(q, kp, vp, table, cu.tolist(), kv.tolist(), scale, torch.zeros_like(q))
+    if what == "a row of q":
+        q[row, 0] = float("nan")
+    elif what == "a channel of q":
+        q[row, G - 1, 7] = float("inf")
+    elif what == "many keys":
+        kp[table[last, :kv_lens[last] // 32].long()] = float("nan")  # the first half, whole pages
+    else:
+        kp[table[last, 3].long(), 0, 5, 9] = float("inf")
+    ref = softmax_rows(q, kp, vp, table, cu.tolist(), kv.tolist(), scale)
+    ws = g.alloc_paged_workspace(g.paged_dims_of(q, kp, table), DEV)
+    out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, scale, max(q_lens), workspace=ws)
+    torch.cuda.synchronize()
+    assert g.device_status() == 0 and int(ws[:4096].count_nonzero()) == 0
+    assert ref.isnan().any() and torch.equal(out.isnan(), ref.isnan())
+    fine = ~ref.isnan()
+    # a key whose score is -inf takes part in no finite row: the others then weigh a little more than the tolerance counts with
+    assert ((out.double() - ref).abs() <= 2 * tol)[fine].all()
