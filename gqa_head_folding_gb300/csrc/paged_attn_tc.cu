@@ -507,7 +507,8 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 const int first0 = w.local * kPagedTile, len = w.s.len;
                 const int lim = pos0 + (rho >> p.gshift);           // this row's
                 const int lim_lo = pos0 + ((r0 + (warp & 3) * 32) >> p.gshift);  // the warp's least
-                float ref = -INFINITY, l = 0.f;
+                // a row behind the item's weighs nothing and never has its reference moved, so that no other depends on it
+                float ref = live ? -INFINITY : INFINITY, l = 0.f;
                 for (int k = 0; k < nx; ++k) {
                     const int jj = dual ? k : 2 * k + g;             // tile within the segment
                     const int tile0 = first0 + jj * kPagedTile;      // its first token
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                             return t.x + t.y;
                         };
                         float cs = 0.f;
-                        const bool fresh = __all_sync(0xffffffffu, ref == -INFINITY);  // of both warps: they share ref
+                        const bool fresh = __all_sync(0xffffffffu, fabsf(ref) == INFINITY);  // of both warps: they share ref
                         // one copy of the exponentials serves both passes: the second, after a
                         // row's reference has moved, is rare, and code that is jumped over costs fetches
 #pragma unroll 1

@@ -149,3 +149,23 @@ def test_attn_nan_and_infinity_reach_the_rows_that_see_them(dtype, q_lens, kv_le
     fine = ~ref.isnan()
     # a key whose score is -inf takes part in no finite row: the others then weigh a little more than the tolerance counts with
     assert ((out.double() - ref).abs() <= 2 * tol)[fine].all()
+
+
+# ---------------------------------------------------------------------------
+# Rows that are no token of the item's request
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("q_lens, kv_lens, G", [([9, 30], [2000, 1500], 2), ([60], [1900], 4), ([150, 3], [800, 900], 1), ([3, 20], [900, 700], 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_does_not_depend_on_other_rows(q_lens, kv_lens, G, D):
+    """Bit for bit the same whatever the rows behind the requests, and the rows of the other requests, hold."""
+    q, kp, vp, table, cu, kv = paged_inputs(q_lens, kv_lens, 2 * G, 2, D, 16, torch.float16, 13, DEV, rows_behind=140)
+    n = q_lens[0]
+    outs = []
+    for fill in (0.0, 1.0, 30.0, float("nan")):
+        x = q.clone()
+        x[n:] = x[n:] * fill if fill == fill else fill
+        outs.append(g.gqa_paged_attn(x, kp, vp, table, cu, kv, 1.0, max(q_lens))[:n])
+    torch.cuda.synchronize()
+    assert torch.isfinite(outs[0]).all() and g.device_status() == 0
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
