@@ -105,6 +105,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// Bound of a CTA's waits, before it retires, for its own copies and products in
+// flight: far above what any takes, however short the other waits are set.
+constexpr uint64_t kLandNs = 2000000000ull;
+
 // 2-D TMA tile load global -> shared, completion signalled on `bar`.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t x,
                                             int32_t y, uint32_t bar, uint64_t policy) {

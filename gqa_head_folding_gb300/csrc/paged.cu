@@ -403,12 +403,14 @@ __global__ void __launch_bounds__(kAppendThreads + 32, 3) paged_append_kernel(co
                 }
             }
         }
-        if (!ok && lane == 0) {
-            raise_flag(p.status, GQAQ_DEV_TIMEOUT);
-            *abort_flag = 1;
-            // let every copy already issued land before this CTA may retire
+        if (lane == 0) {
+            if (!ok) {
+                raise_flag(p.status, GQAQ_DEV_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every copy issued lands before this CTA may retire, also where a consumer has given up on it
             for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-                mbar_wait(smem_u32(&full[i % p.stages]), (uint32_t)(i / p.stages) & 1u, p.timeout_ns, nullptr);
+                mbar_wait(smem_u32(&full[i % p.stages]), (uint32_t)(i / p.stages) & 1u, kLandNs, nullptr);
         }
         return;
     }

@@ -288,12 +288,14 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
             }
             if (!ok) break;
         } while (w.advance(p.w));
-        if (!ok && lane == 0) {
-            raise_flag(p.status, GQAQ_DEV_TIMEOUT);
-            *abort_flag = 1;
-            // let every copy already issued land before this CTA may retire
+        if (lane == 0) {
+            if (!ok) {
+                raise_flag(p.status, GQAQ_DEV_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every copy issued lands before this CTA may retire, also where a consumer has given up on it
             for (int it = i > C::NSTAGE ? i - C::NSTAGE : 0; it < i; ++it)
-                mbar_wait(smem_u32(&full[it % C::NSTAGE]), (uint32_t)(it / C::NSTAGE) & 1u, p.timeout_ns, nullptr);
+                mbar_wait(smem_u32(&full[it % C::NSTAGE]), (uint32_t)(it / C::NSTAGE) & 1u, kLandNs, nullptr);
         }
         return;
     }

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             uint8_t *ring = is_k ? sk : sv;
             const uint64_t pol = l2_policy_evict_first();
             const int ppt = kPagedTile >> p.w.shift;
-            int seg = 0, i = 0;
+            int seg = 0, i = 0, n_q = 0;  // segments, tiles and Q tiles asked for
             bool ok = true;
             while (more) {
                 const int n = w.seg_len();
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                         ok = warp_mbar_wait_slow(smem_u32(qempty), (uint32_t)(seg - 1) & 1u, p.timeout_ns, abort_flag);
                         if (!ok) break;
                     }
+                    ++n_q;
                     if (lane == 0) {
                         const int nq = rows > 128 ? 2 : 1;
                         mbar_arrive_expect_tx(smem_u32(qfull), (uint32_t)(nq * C::TILE));
@@ -334,15 +335,15 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
                 ++seg;
                 more = w.advance(p.w);
             }
-            if (!ok && lane == 0) {
-                raise_flag(p.status, GQAQ_DEV_TIMEOUT);
-                *abort_flag = 1;
-                // let every copy already issued land before this CTA may retire
+            if (lane == 0) {
+                if (!ok) {
+                    raise_flag(p.status, GQAQ_DEV_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                // every copy issued lands before this CTA may retire, also where another warp has given up on it
                 for (int it = i > NS ? i - NS : 0; it < i; ++it)
-                    mbar_wait(smem_u32(&full[it % NS]), (uint32_t)(it / NS) & 1u, p.timeout_ns, nullptr);
-                if (is_k)
-                    for (int it = seg > 1 ? seg - 1 : 0; it <= seg; ++it)  // Q of this segment, if it was asked for
-                        mbar_wait(smem_u32(qfull), (uint32_t)it & 1u, p.timeout_ns / 8, nullptr);
+                    mbar_wait(smem_u32(&full[it % NS]), (uint32_t)(it / NS) & 1u, kLandNs, nullptr);
+                if (n_q > 0) mbar_wait(smem_u32(qfull), (uint32_t)(n_q - 1) & 1u, kLandNs, nullptr);
             }
         } else if (warp == 17) {
             // --------------------------------------------------------------
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
             }
             __syncwarp();
             warp_commit(smem_u32(drain));  // every issued MMA completes before TMEM is released
-            mbar_wait(smem_u32(drain), 0u, p.timeout_ns, nullptr);
+            mbar_wait(smem_u32(drain), 0u, kLandNs, nullptr);
             __syncwarp();
         } else if (warp == 19) {
             // --------------------------------------------------------------

@@ -169,3 +169,43 @@ def test_attn_does_not_depend_on_other_rows(q_lens, kv_lens, G, D):
     assert torch.isfinite(outs[0]).all() and g.device_status() == 0
     for out in outs[1:]:
         assert torch.equal(out, outs[0])
+
+
+# ---------------------------------------------------------------------------
+# Waits that run out while copies and products are in flight
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("ns", [0, 500, 4000])
+@pytest.mark.parametrize("q_lens, kv_lens", [([1, 1], [300, 3000]), ([40], [3000]), ([200, 3], [900, 500])])
+def test_short_waits_leave_nothing_in_flight(q_lens, kv_lens, ns):
+    """Every wait gives up after ns: the call ends, the counters are zero and the next call is right."""
+    q, kp, vp, table, cu, kv = paged_inputs(q_lens, kv_lens, 4, 2, 128, 16, torch.float16, 6, DEV)
+    ref, tol = ref_attn(q, kp, vp, table, cu.tolist(), kv.tolist(), 0.09, torch.zeros_like(q))
+    ws = g.alloc_paged_workspace(g.paged_dims_of(q, kp, table), DEV)
+    g.set_option(g.GQAQ_OPT_WAIT_TIMEOUT_NS, ns)
+    for _ in range(4):
+        g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.09, max(q_lens), workspace=ws)
+    torch.cuda.synchronize()
+    assert g.device_status() in (0, g.GQAQ_DEV_TIMEOUT)  # a wait whose barrier was ready in time did not run out
+    g.set_option(g.GQAQ_OPT_WAIT_TIMEOUT_NS, 2_000_000_000)
+    assert int(ws[:4096].count_nonzero()) == 0
+    out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.09, max(q_lens), workspace=ws)
+    torch.cuda.synchronize()
+    assert ((out.double() - ref).abs() <= tol).all() and g.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [3, 3000])
+def test_short_waits_of_the_append(T):
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    q, k, v = (torch.randn(T, h, 128, generator=gen, device=DEV).half() for h in (8, 2, 2))
+    kp, vp = (torch.zeros(pages_of(T, 16), 2, 16, 128, dtype=torch.float16, device=DEV) for _ in range(2))
+    pos = slots = torch.arange(T, dtype=torch.int32, device=DEV)
+    g.set_option(g.GQAQ_OPT_WAIT_TIMEOUT_NS, 0)
+    for _ in range(4):
+        g.paged_norm_rope_append(q, k, v, pos, slots, kp, vp)
+    torch.cuda.synchronize()
+    assert g.device_status() in (0, g.GQAQ_DEV_TIMEOUT)
+    g.set_option(g.GQAQ_OPT_WAIT_TIMEOUT_NS, 2_000_000_000)
+    out = g.paged_norm_rope_append(q, k, v, pos, slots, kp, vp)
+    torch.cuda.synchronize()
+    rows = lambda p: p.transpose(1, 2).reshape(-1, 2, 128)[:T]  # noqa: E731
+    assert torch.equal(out, q) and torch.equal(rows(kp), k) and torch.equal(rows(vp), v) and g.device_status() == 0
