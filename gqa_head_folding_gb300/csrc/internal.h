@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gqaq.h"
 #include "common.cuh"
 
@@ -146,7 +148,19 @@ int launch_score_pages(const gqaq_dims *dims, const __half *q, const __half *met
 int launch_topk_pages(const gqaq_dims *dims, const float *scores, const int *valid_len, int k,
                       int *page_idx, const LaunchCtx &ctx);
 
+// Lets a kernel use `bytes` of dynamic shared memory on the current device, once: `ready` (the kernel's own, a bit per
+// device) says where it has been. Threads that come here at once set the same value.
+inline int allow_smem(const void *kern, int bytes, std::atomic<uint64_t> &ready, const LaunchCtx &ctx) {
+    if (ctx.device < 0 || ctx.device >= 64) return GQAQ_ERR_UNSUPPORTED;
+    const uint64_t bit = 1ull << ctx.device;
+    if (ready.load(std::memory_order_acquire) & bit) return GQAQ_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return GQAQ_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_release);
+    return GQAQ_OK;
+}
+
 // Paged caches (paged.cu): the step's plan, page release, norm + rotation + append.
+constexpr int kPagedMaxBatch = 8192;  // requests: the prefix sums of the plan fit shared memory
 struct PagedTablesArgs {
     const gqaq_paged_dims *dims;
     const int *cache_len, *new_len, *free_pages, *free_count;

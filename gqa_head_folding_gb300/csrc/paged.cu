@@ -227,12 +227,14 @@ int table_ctas(int64_t work, bool in_place) {
     return c;
 }
 
+// The sums of the largest batch pass the 48 KB that a kernel has without asking (its static shared memory counts too).
+// The limit belongs to the kernel and not to a call, so it is raised once per device, to what any batch takes.
 template <typename P>
-int launch_tables(void (*kern)(P), const P &p, int words, int64_t work, bool in_place, const LaunchCtx &ctx) {
+int launch_tables(void (*kern)(P), const P &p, int words, int most_words, int64_t work, bool in_place, std::atomic<uint64_t> &ready,
+                  const LaunchCtx &ctx) {
     const size_t smem = (size_t)words * sizeof(int);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return GQAQ_ERR_CUDA;
+    const int rc = allow_smem(reinterpret_cast<const void *>(kern), most_words * (int)sizeof(int), ready, ctx);
+    if (rc != GQAQ_OK) return rc;
     const int ctas = table_ctas(work, in_place);
     const cudaError_t e = launch_kernel(kern, dim3((unsigned)ctas), dim3(kTabThreads), smem, ctx, in_place ? ctas : 0, p);
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;
@@ -586,7 +588,9 @@ int launch_paged_tables(const PagedTablesArgs &a, const LaunchCtx &ctx) {
     p.shift = log2_of(d.page_size);
     p.num_pages = d.num_pages;
     p.max_pages = d.max_pages;
-    return launch_tables(paged_tables_kernel, p, 3 * d.batch + 2, (int64_t)d.max_tokens + d.batch, a.free_count == a.free_count_out, ctx);
+    static std::atomic<uint64_t> ready{0};
+    return launch_tables(paged_tables_kernel, p, 3 * d.batch + 2, 3 * kPagedMaxBatch + 2, (int64_t)d.max_tokens + d.batch,
+                         a.free_count == a.free_count_out, ready, ctx);
 }
 
 int launch_paged_release(const PagedReleaseArgs &a, const LaunchCtx &ctx) {
@@ -605,8 +609,9 @@ int launch_paged_release(const PagedReleaseArgs &a, const LaunchCtx &ctx) {
     p.num_pages = d.num_pages;
     p.max_pages = d.max_pages;
     const int64_t table = (int64_t)d.batch * d.max_pages;  // at most this many pages leave, and at most the pool
-    return launch_tables(paged_release_kernel, p, 2 * d.batch + 1, table < d.num_pages ? table : d.num_pages,
-                         a.free_count == a.free_count_out, ctx);
+    static std::atomic<uint64_t> ready{0};
+    return launch_tables(paged_release_kernel, p, 2 * d.batch + 1, 2 * kPagedMaxBatch + 1, table < d.num_pages ? table : d.num_pages,
+                         a.free_count == a.free_count_out, ready, ctx);
 }
 
 int launch_paged_append(const PagedAppendArgs &a, const LaunchCtx &ctx) {

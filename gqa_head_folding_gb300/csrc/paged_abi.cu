@@ -8,7 +8,6 @@ using namespace gqaq;
 
 namespace {
 
-constexpr int kMaxBatch = 8192;        // prefix sums of the plan fit shared memory
 constexpr int kMaxTokens = 1 << 22;
 
 bool page_size_ok(int s) { return s == 8 || s == 16 || s == 32 || s == 64 || s == 128; }
@@ -18,7 +17,7 @@ int check_paged(const gqaq_paged_dims *d, bool heads) {
     if (d == nullptr) return GQAQ_ERR_INVALID_ARG;
     if (d->batch < 1 || d->page_size < 1 || d->num_pages < 1 || d->max_pages < 1 || d->max_tokens < 1)
         return GQAQ_ERR_INVALID_ARG;
-    if (!page_size_ok(d->page_size) || d->batch > kMaxBatch || d->max_tokens > kMaxTokens) return GQAQ_ERR_UNSUPPORTED;
+    if (!page_size_ok(d->page_size) || d->batch > kPagedMaxBatch || d->max_tokens > kMaxTokens) return GQAQ_ERR_UNSUPPORTED;
     // positions, slots and their tiles' ends are 32-bit numbers
     if ((int64_t)d->max_pages * d->page_size > INT32_MAX - 1024 || (int64_t)d->num_pages * d->page_size > INT32_MAX - 1024 ||
         (int64_t)d->batch * d->max_pages > INT32_MAX)

@@ -1,5 +1,10 @@
 """The paged serving calls at their edges: what they refuse or leave as it was, NaN and waits that run out, sizes at a limit, and
 long contexts whose outputs show the loss of a single key."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +15,7 @@ from test_gpu_paged_run import Loop
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def ints(x):
@@ -209,3 +215,58 @@ def test_short_waits_of_the_append(T):
     torch.cuda.synchronize()
     rows = lambda p: p.transpose(1, 2).reshape(-1, 2, 128)[:T]  # noqa: E731
     assert torch.equal(out, q) and torch.equal(rows(kp), k) and torch.equal(rows(vp), v) and g.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# Batches whose sums need more shared memory than a kernel has without asking
+# ---------------------------------------------------------------------------
+CHILD = """
+import sys, torch
+import gqa_head_folding_gb300 as g
+call, B = sys.argv[1], int(sys.argv[2])
+full = lambda n, v: torch.full((n,), v, dtype=torch.int32, device="cuda:0")
+pages = torch.arange(B, dtype=torch.int32, device="cuda:0")
+if call == "plan":
+    kv, cu, pos, slots, count = g.paged_build_tables(full(B, 0), full(B, 1), pages, full(1, B), full(B, -1)[:, None], B, 8)
+    assert int(kv.sum()) == B and int(cu[-1]) == B and count.item() == 0 and torch.equal(slots, 8 * pages.flip(0))
+else:
+    free = full(B, -1)
+    count = g.paged_release_pages(full(B, 1), full(B, 0), pages[:, None].contiguous(), free, full(1, 0), 8)
+    assert count.item() == B and torch.equal(free, pages)
+assert g.device_status() == 0
+"""
+
+
+@pytest.mark.parametrize("call, B", [("plan", 4063), ("plan", 4064), ("plan", 4095), ("plan", 4096), ("release", 6112), ("release", 6143),
+                                     ("release", 6144)])
+def test_batches_in_a_process_of_their_own(call, B):
+    """The first call of a process, where no larger batch has asked for the room before."""
+    r = subprocess.run([sys.executable, "-c", CHILD, call, str(B)], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": ROOT})
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_plans_of_two_threads():
+    """Two host threads plan batches of unlike size on streams of their own."""
+    wrong = []
+
+    def work(B):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                zero, one = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+                pages = torch.arange(B, dtype=torch.int32, device=DEV)
+                count, table = torch.full((1,), B, dtype=torch.int32, device=DEV), torch.zeros(B, 1, dtype=torch.int32, device=DEV)
+                for _ in range(400):
+                    slots = g.paged_build_tables(zero, one, pages, count, table, B, 8)[3]
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(slots, 8 * pages.flip(0)):
+                    wrong.append(B)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in (8192, 4200, 5000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and g.device_status() == 0
