@@ -539,13 +539,9 @@ int launch_append_t(AppendPagedParams &p, bool inter, const LaunchCtx &ctx) {
     p.stage_bytes = stage(gy);
     p.stages = kAppendRing / p.stage_bytes < kAppendStages ? kAppendRing / p.stage_bytes : kAppendStages;
     const size_t smem = 4 * D + (size_t)p.stages * p.stage_bytes;
-    static bool ready[2][64] = {};
-    if (ctx.device < 0 || ctx.device >= 64) return GQAQ_ERR_UNSUPPORTED;
-    if (!ready[inter][ctx.device]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * D + kAppendRing) != cudaSuccess)
-            return GQAQ_ERR_CUDA;
-        ready[inter][ctx.device] = true;
-    }
+    static std::atomic<uint64_t> ready[2] = {};
+    const int rc = allow_smem(reinterpret_cast<const void *>(kern), 4 * D + kAppendRing, ready[inter], ctx);
+    if (rc != GQAQ_OK) return rc;
     // consumers: the rows in as few passes as 256 threads allow, all full
     const int rows = (H + gy - 1) / gy, lanes = D / 16, passes = (rows * lanes + kAppendThreads - 1) / kAppendThreads;
     const int threads = ((rows + passes - 1) / passes * lanes + 31) / 32 * 32 + 32;

@@ -26,6 +26,8 @@
 // the parts (one request at 4K: 10.3 us).
 #include <math.h>
 
+#include <atomic>
+
 #include "attn_mma.cuh"
 #include "paged_sched.cuh"
 
@@ -437,17 +439,19 @@ __global__ void __launch_bounds__(PdCfg<D>::THREADS, PdCfg<D>::MIN_BLOCKS)
 template <int D, bool BF16>
 int decode_grid(const LaunchCtx &ctx) {
     using C = PdCfg<D>;
-    static int occ[64] = {};
+    // CTAs per SM, asked for once per device
+    static std::atomic<int> occ[64] = {};
     if (ctx.device < 0 || ctx.device >= 64) return -1;
-    if (occ[ctx.device] == 0) {
-        int n = 0;
+    int per_sm = occ[ctx.device].load(std::memory_order_acquire);
+    if (per_sm == 0) {
         auto kern = paged_decode_kernel<D, BF16>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, C::THREADS, C::SMEM) != cudaSuccess || n < 1)
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::THREADS, C::SMEM) != cudaSuccess || per_sm < 1)
             return -1;
-        occ[ctx.device] = n < C::MIN_BLOCKS ? n : C::MIN_BLOCKS;
+        if (per_sm > C::MIN_BLOCKS) per_sm = C::MIN_BLOCKS;
+        occ[ctx.device].store(per_sm, std::memory_order_release);
     }
-    const int grid = occ[ctx.device] * ctx.num_sms;
+    const int grid = per_sm * ctx.num_sms;
     return ctx.max_ctas > 0 && ctx.max_ctas < grid ? ctx.max_ctas : grid;
 }
 

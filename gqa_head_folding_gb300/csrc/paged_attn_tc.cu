@@ -791,18 +791,13 @@ __global__ void __launch_bounds__(PtcCfg<D>::THREADS, 1)
 template <int D, bool BF16>
 int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     using C = PtcCfg<D>;
-    static bool ready[64] = {};
-    if (ctx.device < 0 || ctx.device >= 64) return GQAQ_ERR_UNSUPPORTED;
-    if (!ready[ctx.device]) {
-        if (cudaFuncSetAttribute(paged_tc_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-            return GQAQ_ERR_CUDA;
-        ready[ctx.device] = true;
-    }
+    static std::atomic<uint64_t> ready{0};
+    const int rc = allow_smem(reinterpret_cast<const void *>(paged_tc_kernel<D, BF16>), C::SMEM, ready, ctx);
+    if (rc != GQAQ_OK) return rc;
     const gqaq_paged_dims &d = *a.dims;
     const int grid = paged_tc_grid(ctx);
     const uint64_t rows = (uint64_t)d.num_pages * d.num_kv_heads * d.page_size;
     PtcParams p;
-    
     p.G = d.num_q_heads / d.num_kv_heads;
     p.gshift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3;
     fill_paged_work(a, 8 - p.gshift, 128 >> p.gshift, kItemTiles, p.w);  // blocks of 256 rows; above 128 a tile runs twice

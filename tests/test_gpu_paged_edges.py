@@ -270,3 +270,39 @@ def test_plans_of_two_threads():
     for t in threads:
         t.join()
     assert not wrong and g.device_status() == 0
+
+
+def test_first_calls_of_many_threads():
+    """The first append and attention of a process, from eight host threads at once."""
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300, env={**os.environ, "PYTHONPATH": ROOT})
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+FIRST = """
+import threading, torch
+import gqa_head_folding_gb300 as g
+wrong, gate = [], threading.Barrier(8)
+def work(i):
+    try:
+        torch.cuda.set_device(0)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            n = 1 if i % 2 else 40
+            q, k, v = (torch.ones(n, h, 64, dtype=torch.float16, device="cuda:0") for h in (4, 2, 2))
+            kp, vp = (torch.zeros(4, 2, 16, 64, dtype=torch.float16, device="cuda:0") for _ in range(2))
+            at = torch.arange(n, dtype=torch.int32, device="cuda:0")
+            table = torch.arange(3, dtype=torch.int32, device="cuda:0")[None]
+            cu, kv = torch.tensor([0, n], dtype=torch.int32, device="cuda:0"), torch.tensor([n], dtype=torch.int32, device="cuda:0")
+            torch.cuda.current_stream().synchronize()
+            gate.wait()
+            q = g.paged_norm_rope_append(q, k, v, at, at, kp, vp)
+            out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.125, n)
+            torch.cuda.current_stream().synchronize()
+            if not bool((out == 1).all()):
+                wrong.append(i)
+    except Exception as e:
+        wrong.append(e)
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not wrong and g.device_status() == 0, wrong
+"""
