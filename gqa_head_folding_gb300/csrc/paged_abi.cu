@@ -9,6 +9,7 @@ using namespace gqaq;
 namespace {
 
 constexpr int kMaxTokens = 1 << 22;
+constexpr int64_t kMaxHeads = 1 << 20;  // q, k and v heads of a token: the append's grid and the bytes of its ring are 32-bit numbers
 
 bool page_size_ok(int s) { return s == 8 || s == 16 || s == 32 || s == 64 || s == 128; }
 
@@ -26,6 +27,7 @@ int check_paged(const gqaq_paged_dims *d, bool heads) {
     if (d->num_q_heads < 1 || d->num_kv_heads < 1 || d->head_dim < 1) return GQAQ_ERR_INVALID_ARG;
     if (d->num_q_heads % d->num_kv_heads != 0) return GQAQ_ERR_INVALID_ARG;
     if (d->dtype != GQAQ_F16 && d->dtype != GQAQ_BF16) return GQAQ_ERR_UNSUPPORTED;
+    if ((int64_t)d->num_q_heads + 2 * (int64_t)d->num_kv_heads > kMaxHeads) return GQAQ_ERR_UNSUPPORTED;
     const int G = d->num_q_heads / d->num_kv_heads;
     if (G != 1 && G != 2 && G != 4 && G != 8) return GQAQ_ERR_UNSUPPORTED;
     if (d->head_dim != 64 && d->head_dim != 128) return GQAQ_ERR_UNSUPPORTED;

@@ -371,9 +371,9 @@ GQAQ_API int gqa_prefill_attn(const gqaq_dims *dims, int q_len, const gqaq_half 
  *
  * q, k, v, out and the pages are fp16 or bfloat16 (dims.dtype, passed as
  * gqaq_half bits). Supported: D in {64, 128}; G in {1, 2, 4, 8}; S in
- * {8, 16, 32, 64, 128}; B <= 8192; max_tokens <= 2^22; max_pages * S,
- * B * max_pages and num_pages * Hkv * S below 2^31 - 1024; max_tokens * Hq
- * below 2^30. Else GQAQ_ERR_UNSUPPORTED.
+ * {8, 16, 32, 64, 128}; B <= 8192; max_tokens <= 2^22; max_pages * S and
+ * num_pages * Hkv * S at most 2^31 - 1025, B * max_pages below 2^31;
+ * max_tokens * Hq below 2^30; Hq + 2 Hkv <= 2^20. Else GQAQ_ERR_UNSUPPORTED.
  *
  * As for every call, what lies on the device is checked there: lengths,
  * positions, slots and page indices out of range are clamped or skipped and

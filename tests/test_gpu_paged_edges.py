@@ -11,6 +11,7 @@ import torch
 
 import gqa_head_folding_gb300 as g
 from _paged import DTYPES, pages_of, paged_inputs, ref_attn, ref_release
+from test_gpu_paged import append_case
 from test_gpu_paged_run import Loop
 
 pytestmark = pytest.mark.gpu
@@ -306,3 +307,8 @@ threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
 [t.join() for t in threads]
 assert not wrong and g.device_status() == 0, wrong
 """
+
+
+@pytest.mark.parametrize("Hq, Hkv", [(4096, 512), (1, 1), (30000, 30000)])
+def test_append_many_heads(Hq, Hkv):
+    append_case(2, Hq, Hkv, 64, 8, "f16", 64, False, True, True, seed=Hq)

@@ -112,3 +112,11 @@ def test_bindings_refuse_cpu_tensors_and_types():
         g.gqa_paged_attn(q, kp, kp, torch.zeros(4, 3, dtype=torch.int32), torch.zeros(5, dtype=torch.int32), i, 0.1, 1)
     with pytest.raises(ValueError, match="bfloat16"):
         g.make_paged_dims(1, 8, 2, 64, 16, 10, 10, 1, torch.float32)
+
+
+@pytest.mark.parametrize("q, kv, status", [(1 << 19, 1 << 18, 1), ((1 << 19) + 2, (1 << 18) + 1, 2), (1 << 23, 1 << 23, 2), (1 << 29, 1 << 26, 2)])
+def test_head_counts_are_limited(q, kv, status):
+    """2^20 heads in all pass on to the next check (a missing pointer), more do not."""
+    d = dims(num_q_heads=q, num_kv_heads=kv, num_pages=1, page_size=8, max_tokens=1)
+    assert append(L=g.lib(), d=d, q=None, sq=1 << 40, sk=1 << 40, sv=1 << 40) == status
+    assert attn(g.lib(), d, q=None) == status
