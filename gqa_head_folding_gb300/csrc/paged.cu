@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kTabThreads) paged_release_kernel(const Releas
         cum[b] = (int)min(at, space);
         at += n;
     }
-    if (all > space) {
+    const bool fits = all <= space;
+    if (!fits) {
         flags |= GQAQ_DEV_BAD_LEN;
         all = space;
     }
@@ -205,7 +206,12 @@ __global__ void __launch_bounds__(kTabThreads) paged_release_kernel(const Releas
     const int stride = nctas * nthreads;
     for (int j = rank * nthreads + tid; j < (int)all; j += stride) {
         const int b = owner_of(cum, p.B, j);
-        p.free_pages[count + j] = p.table[(int64_t)b * p.max_pages + from[b] + (j - cum[b])];
+        int page = p.table[(int64_t)b * p.max_pages + from[b] + (j - cum[b])];
+        if (fits && (page < 0 || page >= p.num_pages)) {  // its place stays, so that the others' follow from the sums alone
+            page = -1;
+            flags |= GQAQ_DEV_BAD_PAGE;
+        }
+        p.free_pages[count + j] = page;
     }
     if (flags) raise_flag(p.status, flags);
     cluster_sync_all();

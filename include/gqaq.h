@@ -427,11 +427,14 @@ GQAQ_API int paged_build_tables(const gqaq_paged_dims *dims, const int32_t *cach
  * free_pages behind the first *free_count entries, in order of (request,
  * page). block_table is not changed: its entries past the kept length are no
  * longer the request's. A page that two rows share goes to the list once for
- * each row that releases it: release shared pages with one row only. free_count_out [1] (may be free_count itself) becomes
- * the new count. A request with keep_len outside [0, kv_len] or kv_len
- * outside [0, max_pages * S] keeps all its pages and raises
- * GQAQ_DEV_BAD_LEN; pages that would pass the end of free_pages are dropped
- * and raise GQAQ_DEV_BAD_LEN. Uses B, S, num_pages and max_pages of dims. */
+ * each row that releases it: release shared pages with one row only. An entry
+ * outside [0, num_pages) raises GQAQ_DEV_BAD_PAGE and its place on the list
+ * holds -1 (which the plan reports again when it comes to it).
+ * free_count_out [1] (may be free_count itself) becomes the new count. A
+ * request with keep_len outside [0, kv_len] or kv_len outside
+ * [0, max_pages * S] keeps all its pages and raises GQAQ_DEV_BAD_LEN. Where the pages that leave pass the end of free_pages,
+ * those that fit are taken as they stand, the others are dropped, and the call
+ * raises GQAQ_DEV_BAD_LEN. Uses B, S, num_pages and max_pages of dims. */
 GQAQ_API int paged_release_pages(const gqaq_paged_dims *dims, const int32_t *kv_len, const int32_t *keep_len,
                                  const int32_t *block_table, int32_t *free_pages, const int32_t *free_count,
                                  int32_t *free_count_out, void *stream);

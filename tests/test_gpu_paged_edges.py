@@ -312,3 +312,19 @@ assert not wrong and g.device_status() == 0, wrong
 @pytest.mark.parametrize("Hq, Hkv", [(4096, 512), (1, 1), (30000, 30000)])
 def test_append_many_heads(Hq, Hkv):
     append_case(2, Hq, Hkv, 64, 8, "f16", 64, False, True, True, seed=Hq)
+
+
+# ---------------------------------------------------------------------------
+# Bad pages
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("in_place", [True, False])
+def test_release_reports_bad_pages(in_place):
+    table = ints([[5, -1, 4], [6, 2, 9], [2 ** 31 - 1, -2 ** 31, 0]])
+    free, count = ints([3] + [-9] * 5), ints([1])
+    out = g.paged_release_pages(ints([32, 32, 33]), ints([0, 3, 17]), table, free, count, 16, free_count_out=count if in_place else None)
+    assert free.tolist() == [3, 5, -1, 2, 0, -9] and out.item() == 5 and g.device_status() == g.GQAQ_DEV_BAD_PAGE
+    free, count = ints([3] + [-9] * 5), ints([1])
+    g.paged_release_pages(ints([32, 32, 33]), ints([16, 16, 33]), table, free, count, 16)
+    assert free.tolist() == [3, -1, 2, -9, -9, -9] and g.device_status() == g.GQAQ_DEV_BAD_PAGE
+    g.paged_release_pages(ints([16, 32, 33]), ints([0, 16, 33]), table, free, count, 16)  # bad entries that are not released
+    assert free.tolist() == [3, 5, 2, -9, -9, -9] and g.device_status() == 0
