@@ -72,7 +72,7 @@ class Dims(ctypes.Structure):
 
 class PagedDims(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int) for name in ("batch", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
-                                                  "num_pages", "max_pages", "max_tokens", "dtype")]
+                                                  "num_pages", "max_pages", "max_tokens", "dtype", "max_len")]
 
 
 # Exported symbols, in the order include/gqaq.h declares them.
@@ -665,12 +665,13 @@ _PAGED_DTYPES = {torch.float16: GQAQ_F16, torch.bfloat16: GQAQ_BF16}
 
 
 def make_paged_dims(batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages, max_tokens,
-                    dtype=torch.float16) -> PagedDims:
-    """Shape of a paged step; dtype is torch.float16 or torch.bfloat16."""
+                    dtype=torch.float16, max_len: int = 0) -> PagedDims:
+    """Shape of a paged step; dtype is torch.float16 or torch.bfloat16. max_len limits a request's tokens in the
+    plan (0: what max_pages hold)."""
     if dtype not in _PAGED_DTYPES:
         raise ValueError(f"paged caches hold torch.float16 or torch.bfloat16, not {dtype}")
     return PagedDims(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size), int(num_pages),
-                     int(max_pages), int(max_tokens), _PAGED_DTYPES[dtype])
+                     int(max_pages), int(max_tokens), _PAGED_DTYPES[dtype], int(max_len))
 
 
 def paged_dims_of(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor) -> PagedDims:
@@ -755,11 +756,12 @@ _cuda_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.
 
 def paged_build_tables(cache_len, new_len, free_pages, free_count, block_table, max_tokens: int,
                        page_size: int = PAGE_SIZE, kv_len=None, cu_q=None, positions=None, slots=None,
-                       free_count_out=None):
+                       free_count_out=None, max_len: int = 0):
     """Plan a paged step on the GPU from cache_len / new_len [B]: take pages off the end of
     free_pages[:free_count], write them to block_table [B,max_pages], and return
     (kv_len [B], cu_q [B+1], positions [max_tokens], slots [max_tokens], free_count_out [1]), all int32.
     Requests are served in order, each wholly or not at all; a refused one has kv_len 0 and slots -1.
+    max_len is the most tokens of a request (0: what its row of block_table holds).
     free_count_out may be free_count itself; without it a new tensor holds the count."""
     i32 = torch.int32
     (B,) = _paged_dim("cache_len", cache_len, 1)
@@ -778,7 +780,7 @@ def paged_build_tables(cache_len, new_len, free_pages, free_count, block_table, 
     if free_count_out is None:
         free_count_out = torch.empty(one, dtype=i32, device=cache_len.device)
     status = lib().paged_build_tables(
-        _paged_dims_ref(B, 0, 0, 0, int(page_size), pool, width, T, 0),
+        _paged_dims_ref(B, 0, 0, 0, int(page_size), pool, width, T, 0, int(max_len)),
         _paged("cache_len", cache_len, i32, per_b, dev), _paged("new_len", new_len, i32, per_b, dev),
         _paged("free_pages", free_pages, i32, (pool,), dev), _paged("free_count", free_count, i32, one, dev),
         _paged("block_table", block_table, i32, (B, width), dev), _paged("kv_len", kv_len, i32, per_b, dev),

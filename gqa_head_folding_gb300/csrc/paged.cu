@@ -55,6 +55,7 @@ struct TablesParams {
     int *table, *kv_len, *cu_q, *positions, *slots, *free_count_out;
     int *status;
     int B, T, S, shift, num_pages, max_pages;
+    int room;  // tokens of a request at most
 };
 
 // Every CTA repeats the two prefix sums over the requests (new
@@ -81,7 +82,6 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
 
     const int per = (p.B + nthreads - 1) / nthreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    const int64_t room = (int64_t)p.max_pages * p.S;
     int64_t rows = 0, all;
     for (int b = b0; b < b1; ++b) rows += max(p.new_len[b], 0);
     rows = block_exclusive(rows, buf, all);
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
         const int64_t c = p.cache_len[b], n = max(p.new_len[b], 0);
         cu[b] = (int)min(rows, (int64_t)p.T);
         rows += n;
-        bool ok = c >= 0 && p.new_len[b] >= 0 && c + n <= room;
+        bool ok = c >= 0 && p.new_len[b] >= 0 && c + n <= p.room;
         if (!ok) flags |= GQAQ_DEV_BAD_LEN;
         if (rows > p.T) {
             ok = false;
@@ -590,6 +590,8 @@ int launch_paged_tables(const PagedTablesArgs &a, const LaunchCtx &ctx) {
     p.shift = log2_of(d.page_size);
     p.num_pages = d.num_pages;
     p.max_pages = d.max_pages;
+    const int held = d.max_pages * d.page_size;
+    p.room = d.max_len > 0 && d.max_len < held ? d.max_len : held;
     static std::atomic<uint64_t> ready{0};
     return launch_tables(paged_tables_kernel, p, 3 * d.batch + 2, 3 * kPagedMaxBatch + 2, (int64_t)d.max_tokens + d.batch,
                          a.free_count == a.free_count_out, ready, ctx);

@@ -16,7 +16,8 @@ bool page_size_ok(int s) { return s == 8 || s == 16 || s == 32 || s == 64 || s =
 // Shape checks of the tables (heads: also of the rows and the pools).
 int check_paged(const gqaq_paged_dims *d, bool heads) {
     if (d == nullptr) return GQAQ_ERR_INVALID_ARG;
-    if (d->batch < 1 || d->page_size < 1 || d->num_pages < 1 || d->max_pages < 1 || d->max_tokens < 1)
+    if (d->batch < 1 || d->page_size < 1 || d->num_pages < 1 || d->max_pages < 1 || d->max_tokens < 1 ||
+        d->max_len < 0)
         return GQAQ_ERR_INVALID_ARG;
     if (!page_size_ok(d->page_size) || d->batch > kPagedMaxBatch || d->max_tokens > kMaxTokens) return GQAQ_ERR_UNSUPPORTED;
     // positions, slots and their tiles' ends are 32-bit numbers

@@ -33,7 +33,7 @@ class PagedCache:
 
     def __init__(self, num_layers: int, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, pool_pages: int,
                  max_len: int, max_tokens: int, device, page_size: int = PAGE_SIZE, dtype=torch.float16):
-        self.device, self.page_size, self.max_tokens = torch.device(device), page_size, max_tokens
+        self.device, self.page_size, self.max_len, self.max_tokens = torch.device(device), page_size, max_len, max_tokens
         self.scale = 1.0 / math.sqrt(head_dim)
         width = num_pages(max_len, page_size)
         dims = make_paged_dims(batch, num_q_heads, num_kv_heads, head_dim, page_size, pool_pages, width, max_tokens, dtype)
@@ -53,10 +53,11 @@ class PagedCache:
 
     def plan(self, new_len: torch.Tensor):
         """Place the step's new_len [batch] tokens. A request the pool has no pages for is refused
-        (kv_len 0, GQAQ_DEV_NO_PAGES): its rows of the step have no effect and out is 0 there."""
+        (kv_len 0, GQAQ_DEV_NO_PAGES), and so is one that would pass max_len (GQAQ_DEV_BAD_LEN): its rows
+        of the step have no effect and out is 0 there."""
         paged_build_tables(self.cache_len, new_len, self.free_pages, self.free_count, self.block_table, self.max_tokens,
                            self.page_size, kv_len=self.kv_len, cu_q=self.cu_q, positions=self.positions, slots=self.slots,
-                           free_count_out=self.free_count)
+                           free_count_out=self.free_count, max_len=self.max_len)
 
     def append(self, layer: int, q, k, v, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
                interleaved: bool = False, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -391,6 +391,7 @@ typedef struct {
     int max_pages;    /* columns of block_table */
     int max_tokens;   /* T >= 1: rows of the step's token arrays */
     int dtype;        /* GQAQ_F16 or GQAQ_BF16 */
+    int max_len;      /* the plan's limit on a request's tokens; 0: what max_pages hold */
 } gqaq_paged_dims;
 
 /* Plan a step on the GPU: from the requests' lengths, the pages they need,
@@ -410,7 +411,8 @@ typedef struct {
  * Requests are served in order, each wholly or not at all: one whose pages
  * (with those of all requests before it) exceed the free ones is refused and
  * raises GQAQ_DEV_NO_PAGES; its row of block_table keeps what it held.
- * Negative lengths, and lengths past max_pages * S, refuse the request with
+ * Negative lengths, and lengths past max_pages * S or max_len (where it is not
+ * 0: the positions of a table of angles, say), refuse the request with
  * GQAQ_DEV_BAD_LEN (a negative new_len counts as no rows); rows past T do so
  * with GQAQ_DEV_BAD_POS. A page index outside [0, num_pages), in the table or
  * on the free list, raises GQAQ_DEV_BAD_PAGE and gives its tokens slot -1.

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import gqa_head_folding_gb300 as g
-from _paged import DTYPES, pages_of, paged_inputs, ref_attn, ref_release
+from _paged import DTYPES, angles, pages_of, paged_inputs, ref_attn, ref_release
 from test_gpu_paged import append_case
 from test_gpu_paged_run import Loop
 
@@ -328,3 +328,36 @@ def test_release_reports_bad_pages(in_place):
     assert free.tolist() == [3, -1, 2, -9, -9, -9] and g.device_status() == g.GQAQ_DEV_BAD_PAGE
     g.paged_release_pages(ints([16, 32, 33]), ints([0, 16, 33]), table, free, count, 16)  # bad entries that are not released
     assert free.tolist() == [3, 5, 2, -9, -9, -9] and g.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# A request's most tokens, where they end inside a page
+# ---------------------------------------------------------------------------
+def test_plan_refuses_tokens_past_max_len():
+    args = dict(free_pages=ints([0, 1, 2, 3]), free_count=ints([4]), max_tokens=12, page_size=16)
+    for most, kv in ((20, [0, 20, 3]), (21, [21, 20, 3]), (0, [21, 20, 3]), (1000, [21, 20, 3])):
+        out = g.paged_build_tables(ints([15, 19, 0]), ints([6, 1, 3]), block_table=ints([[3, 0], [3, 2], [0, 0]]), max_len=most, **args)
+        assert out[0].tolist() == kv and out[1].tolist() == [0, 6, 7, 10]  # a refused request's rows are counted
+        assert g.device_status() == (g.GQAQ_DEV_BAD_LEN if kv[0] == 0 else 0)
+    with pytest.raises(g.GqaqError):
+        g.paged_build_tables(ints([0]), ints([1]), block_table=ints([[0, 0]]), max_len=-1, **args)
+
+
+@pytest.mark.parametrize("max_len", [100, 128, 7])
+def test_cache_ends_requests_at_max_len(max_len):
+    """Pages of 64 tokens hold more than max_len; the table of angles does not reach further."""
+    L = Loop(2, 4, 2, 64, 64, torch.float16, 8, max_len, 2 * max_len + 2, seed=5)
+    L.c.plan(ints([max_len + 1, 5]))
+    assert L.c.kv_len.tolist() == [0, 5] and g.device_status() == g.GQAQ_DEV_BAD_LEN
+    assert L.c.slots[:max_len + 1].max() == -1
+    L.c.release(ints([0, 0]))
+    L.free, L.count = L.c.free_pages.cpu().numpy().astype(np.int64), L.c.free_count.item()
+    L.table = L.c.block_table.cpu().numpy().astype(np.int64)
+    assert L.count == 8
+    L.step([max_len - 1, 3])
+    L.step([1, 4])
+    assert g.device_status() == 0 and L.len.tolist() == [max_len, 7]
+    L.c.plan(ints([1, 0]))
+    assert L.c.kv_len.tolist() == [0, 7] and g.device_status() == g.GQAQ_DEV_BAD_LEN
+    L.c.commit()
+    assert L.c.cache_len.tolist() == [max_len, 7]
