@@ -29,7 +29,8 @@ from . import (PAGE_SIZE, alloc_paged_workspace, gqa_paged_attn, make_paged_dims
 class PagedCache:
     """Pools, block table and free list of up to ``batch`` requests of at most ``max_len`` tokens each.
 
-    ``max_tokens`` is the most new tokens of a step (rows behind the step's tokens are padding)."""
+    ``max_tokens`` is the most new tokens of a step. A step's q, k and v have the rows that its plan was
+    given (max_tokens, or fewer); rows behind the step's tokens are padding."""
 
     def __init__(self, num_layers: int, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, pool_pages: int,
                  max_len: int, max_tokens: int, device, page_size: int = PAGE_SIZE, dtype=torch.float16):
@@ -50,24 +51,34 @@ class PagedCache:
         self.cu_q = torch.zeros(batch + 1, **i32)
         self.positions = torch.zeros(max_tokens, **i32)
         self.slots = torch.full((max_tokens,), -1, **i32)
+        self._rows = (self.positions, self.slots)    # of the planned step
 
-    def plan(self, new_len: torch.Tensor):
-        """Place the step's new_len [batch] tokens. A request the pool has no pages for is refused
+    def plan(self, new_len: torch.Tensor, rows: Optional[int] = None):
+        """Place the step's new_len [batch] tokens in as many rows (None: max_tokens). A request that does not
+        fit them is refused (GQAQ_DEV_BAD_POS). A request the pool has no pages for is refused
         (kv_len 0, GQAQ_DEV_NO_PAGES), and so is one that would pass max_len (GQAQ_DEV_BAD_LEN): its rows
         of the step have no effect and out is 0 there."""
-        paged_build_tables(self.cache_len, new_len, self.free_pages, self.free_count, self.block_table, self.max_tokens,
-                           self.page_size, kv_len=self.kv_len, cu_q=self.cu_q, positions=self.positions, slots=self.slots,
+        n = self.max_tokens if rows is None else int(rows)
+        if not 1 <= n <= self.max_tokens:
+            raise ValueError(f"rows must lie in 1 .. max_tokens = {self.max_tokens}, got {n}")
+        positions, slots = self.positions[:n], self.slots[:n]
+        paged_build_tables(self.cache_len, new_len, self.free_pages, self.free_count, self.block_table, n, self.page_size,
+                           kv_len=self.kv_len, cu_q=self.cu_q, positions=positions, slots=slots,
                            free_count_out=self.free_count, max_len=self.max_len)
+        self._rows = (positions, slots)
 
     def append(self, layer: int, q, k, v, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
                interleaved: bool = False, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """The layer's projected q [max_tokens,Hq,D] and k, v [max_tokens,Hkv,D]: returns q for attend."""
-        return paged_norm_rope_append(q, k, v, self.positions, self.slots, self.k_pages[layer], self.v_pages[layer],
+        """The layer's projected q [rows,Hq,D] and k, v [rows,Hkv,D]: returns q for attend."""
+        positions, slots = self._rows
+        return paged_norm_rope_append(q, k, v, positions, slots, self.k_pages[layer], self.v_pages[layer],
                                       q_weight=q_weight, k_weight=k_weight, eps=eps, cos_sin=cos_sin, interleaved=interleaved,
                                       q_out=q_out)
 
     def attend(self, layer: int, q, max_q_len: int, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """Attention of the step's tokens; max_q_len bounds the new tokens of a request."""
+        """Attention of the step's tokens, q [rows,Hq,D]; max_q_len bounds the new tokens of a request."""
+        if q.shape[0] != self._rows[0].shape[0]:
+            raise ValueError(f"q must have the {self._rows[0].shape[0]} rows of the step's plan, got {q.shape[0]}")
         return gqa_paged_attn(q, self.k_pages[layer], self.v_pages[layer], self.block_table, self.cu_q, self.kv_len, self.scale,
                               max_q_len, out=out, workspace=self.workspace)
 

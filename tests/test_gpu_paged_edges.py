@@ -11,6 +11,7 @@ import torch
 
 import gqa_head_folding_gb300 as g
 from _paged import DTYPES, angles, pages_of, paged_inputs, ref_attn, ref_release
+from gqa_head_folding_gb300.paged import PagedCache
 from test_gpu_paged import append_case
 from test_gpu_paged_run import Loop
 
@@ -361,3 +362,46 @@ def test_cache_ends_requests_at_max_len(max_len):
     assert L.c.kv_len.tolist() == [0, 7] and g.device_status() == g.GQAQ_DEV_BAD_LEN
     L.c.commit()
     assert L.c.cache_len.tolist() == [max_len, 7]
+
+
+# ---------------------------------------------------------------------------
+# Steps of fewer rows than the object's most
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_steps_of_few_rows(dtype):
+    """The same steps through projections of max_tokens rows and of the step's own rows."""
+    wide, tight = (PagedCache(1, 3, 8, 2, 64, 40, 200, 150, DEV, 16, dtype) for _ in range(2))
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    cs = angles(200, 64).to(DEV)
+    for n in ([60, 3, 20], [1, 1, 1], [0, 1, 0], [4, 4, 4], [1, 0, 30]):
+        x = torch.randn(150, 12, 64, generator=gen, device=DEV).to(dtype)
+        rows, outs = sum(n), []
+        for c, t in ((wide, None), (tight, rows)):
+            q, k, v = x[:t].split([8, 2, 2], dim=1)
+            c.plan(ints(n), t)
+            out = c.attend(0, c.append(0, q, k, v, cos_sin=cs), max(n))
+            c.commit()
+            outs.append(out[:rows])
+        assert outs[1].shape[0] == rows and torch.equal(*outs) and torch.equal(wide.slots[:rows], tight.slots[:rows])
+        for a, b in ((wide.cache_len, tight.cache_len), (wide.block_table, tight.block_table), (wide.free_count, tight.free_count)):
+            assert torch.equal(a, b)
+    assert g.device_status() == 0
+
+
+def test_steps_of_few_rows_refusals():
+    c = PagedCache(1, 2, 4, 2, 64, 10, 64, 30, DEV)
+    q, k, v = (torch.zeros(30, h, 64, dtype=torch.float16, device=DEV) for h in (4, 2, 2))
+    for rows in (0, -1, 31):
+        with pytest.raises(ValueError):
+            c.plan(ints([1, 1]), rows)
+    c.plan(ints([3, 9]), 8)          # 12 tokens in 8 rows
+    assert g.device_status() == g.GQAQ_DEV_BAD_POS and c.kv_len.tolist() == [3, 0]
+    for n in (7, 9, 30):             # rows behind the plan's hold what an earlier step left
+        with pytest.raises(ValueError):
+            c.append(0, q[:n], k[:n], v[:n])
+    c.append(0, q[:8], k[:8], v[:8])
+    with pytest.raises(ValueError):
+        c.attend(0, q, 3)
+    c.attend(0, q[:8], 3)            # the refused request's five rows are above the bound
+    c.commit()
+    assert g.device_status() == g.GQAQ_DEV_BAD_LEN and c.cache_len.tolist() == [3, 0]
