@@ -43,6 +43,7 @@ GQAQ_DEV_NO_PAGES = 16
 
 GQAQ_F16 = 0
 GQAQ_BF16 = 1
+GQAQ_PAGED_COUNTER_BYTES = 4096
 
 GQAQ_OPT_MAX_CTAS = 1
 GQAQ_OPT_WAIT_TIMEOUT_NS = 2
@@ -689,9 +690,11 @@ def paged_workspace_bytes(dims: PagedDims) -> int:
 
 
 def alloc_paged_workspace(dims: PagedDims, device) -> torch.Tensor:
-    """Zero-filled workspace for gqa_paged_attn (its counters stay zero between calls).
+    """Workspace for gqa_paged_attn, its counters zero (they stay so between calls; what follows them holds anything).
     Its size depends on head_dim and the device only, so one serves every batch and every layer in a stream."""
-    return torch.zeros(paged_workspace_bytes(dims), dtype=torch.uint8, device=device)
+    workspace = torch.empty(paged_workspace_bytes(dims), dtype=torch.uint8, device=device)
+    workspace[:GQAQ_PAGED_COUNTER_BYTES].zero_()
+    return workspace
 
 
 def new_pages(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device,

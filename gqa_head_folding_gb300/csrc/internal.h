@@ -200,7 +200,7 @@ int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx);
 size_t paged_attn_workspace_bytes(const gqaq_paged_dims *dims, const LaunchCtx &ctx);
 // Its kernels. The workspace holds arrival counters (one word per CTA, zero
 // between calls) in its first kPagedCountBytes, then the partials.
-constexpr size_t kPagedCountBytes = 4096;
+constexpr size_t kPagedCountBytes = GQAQ_PAGED_COUNTER_BYTES;
 int paged_tc_grid(const LaunchCtx &ctx);
 int launch_paged_tc(const PagedAttnArgs &a, const LaunchCtx &ctx);
 size_t paged_tc_workspace_bytes(const gqaq_paged_dims *dims, const LaunchCtx &ctx);

@@ -472,7 +472,9 @@ GQAQ_API int paged_norm_rope_append(const gqaq_paged_dims *dims, const gqaq_half
 
 /* Bytes of workspace gqa_paged_attn needs on the current device. Depends on
  * D and the SM count only; 0 when dims are invalid or unsupported. Zero-fill
- * it once; every call leaves its counters at zero. */
+ * its first GQAQ_PAGED_COUNTER_BYTES once (counters, which every call leaves at
+ * zero); the rest may hold anything. */
+enum { GQAQ_PAGED_COUNTER_BYTES = 4096 };
 GQAQ_API size_t gqaq_paged_workspace_bytes(const gqaq_paged_dims *dims);
 
 /* Attention of each request's new tokens over its pages: one token, a few
@@ -495,8 +497,8 @@ GQAQ_API size_t gqaq_paged_workspace_bytes(const gqaq_paged_dims *dims);
  * GQAQ_DEV_BAD_LEN; a cu_q entry that descends or leaves [0, T] is clamped
  * and raises GQAQ_DEV_BAD_POS; a page index outside [0, num_pages) raises
  * GQAQ_DEV_BAD_PAGE, and its page reads as zeros.
- * workspace: >= gqaq_paged_workspace_bytes(dims), zero-filled before its
- * first use. Two calls that overlap on the GPU must not share it. */
+ * workspace: >= gqaq_paged_workspace_bytes(dims), its counters zero-filled
+ * before its first use. Two calls that overlap on the GPU must not share it. */
 GQAQ_API int gqa_paged_attn(const gqaq_paged_dims *dims, int max_q_len, const gqaq_half *q, const gqaq_half *k_pages,
                             const gqaq_half *v_pages, const int32_t *block_table, const int32_t *cu_q,
                             const int32_t *kv_len, float scale, gqaq_half *out, void *workspace,

@@ -405,3 +405,23 @@ def test_steps_of_few_rows_refusals():
     c.attend(0, q[:8], 3)            # the refused request's five rows are above the bound
     c.commit()
     assert g.device_status() == g.GQAQ_DEV_BAD_LEN and c.cache_len.tolist() == [3, 0]
+
+
+# ---------------------------------------------------------------------------
+# Workspace and arguments
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [64, 128])
+def test_only_the_counters_of_a_workspace_need_zeros(D):
+    dims = g.make_paged_dims(1, 8, 2, D, 16, 1, 1, 1)
+    n = g.paged_workspace_bytes(dims)
+    torch.full((n,), 255, dtype=torch.uint8, device=DEV)  # what the allocator hands out next has been used
+    ws = g.alloc_paged_workspace(dims, DEV)
+    assert ws.numel() == n and int(ws[:4096].count_nonzero()) == 0
+    ws[4096:] = 255  # NaN as floats
+    for q_lens, kv_lens in (([1, 1], [300, 3000]), ([40], [6000]), ([200, 3], [5900, 500])):
+        q, kp, vp, table, cu, kv = paged_inputs(q_lens, kv_lens, 4, 2, D, 16, torch.float16, 6, DEV)
+        ref, tol = ref_attn(q, kp, vp, table, cu.tolist(), kv.tolist(), 0.09, torch.zeros_like(q))
+        for w in (ws, None):
+            out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.09, max(q_lens), workspace=w)
+            assert ((out.double() - ref).abs() <= tol).all()
+    assert g.device_status() == 0
