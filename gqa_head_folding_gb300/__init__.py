@@ -665,14 +665,22 @@ def new_meta(batch: int, num_kv_heads: int, max_len: int, head_dim: int, device,
 _PAGED_DTYPES = {torch.float16: GQAQ_F16, torch.bfloat16: GQAQ_BF16}
 
 
+def _int32(name: str, value) -> int:
+    """value, where the library's 32-bit argument can hold it (ctypes would cut it short)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def make_paged_dims(batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages, max_tokens,
                     dtype=torch.float16, max_len: int = 0) -> PagedDims:
     """Shape of a paged step; dtype is torch.float16 or torch.bfloat16. max_len limits a request's tokens in the
     plan (0: what max_pages hold)."""
     if dtype not in _PAGED_DTYPES:
         raise ValueError(f"paged caches hold torch.float16 or torch.bfloat16, not {dtype}")
-    return PagedDims(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size), int(num_pages),
-                     int(max_pages), int(max_tokens), _PAGED_DTYPES[dtype], int(max_len))
+    return PagedDims(*(_int32(name, int(value)) for (name, _), value in zip(
+        PagedDims._fields_, (batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, max_pages, max_tokens,
+                             _PAGED_DTYPES[dtype], max_len))))
 
 
 def paged_dims_of(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor) -> PagedDims:
@@ -750,7 +758,7 @@ def _paged_device(name: str, t) -> int:
 @functools.lru_cache(maxsize=1024)
 def _paged_dims_ref(*fields):
     """A pointer to the gqaq_paged_dims with these fields (the library only reads it during the call)."""
-    return ctypes.pointer(PagedDims(*fields))
+    return ctypes.pointer(PagedDims(*(_int32(name, value) for (name, _), value in zip(PagedDims._fields_, fields))))
 
 
 _cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -887,7 +895,8 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, cu_q, kv_len, scale: float,
         workspace = alloc_paged_workspace(dims.contents, q.device)
     (nbytes,) = _paged_dim("workspace", workspace, 1)
     status = lib().gqa_paged_attn(
-        dims, max_q_len, aq, _paged("k_pages", k_pages, dt, pool, dev), _paged("v_pages", v_pages, dt, pool, dev),
+        dims, _int32("max_q_len", max_q_len), aq, _paged("k_pages", k_pages, dt, pool, dev),
+        _paged("v_pages", v_pages, dt, pool, dev),
         _paged("block_table", block_table, i32, (B, max_pages), dev), _paged("cu_q", cu_q, i32, (B + 1,), dev),
         _paged("kv_len", kv_len, i32, (B,), dev), scale, _paged("out", out, dt, rows, dev),
         _paged("workspace", workspace, torch.uint8, (nbytes,), dev), nbytes, _cuda_stream(dev))

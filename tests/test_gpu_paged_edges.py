@@ -425,3 +425,14 @@ def test_only_the_counters_of_a_workspace_need_zeros(D):
             out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.09, max(q_lens), workspace=w)
             assert ((out.double() - ref).abs() <= tol).all()
     assert g.device_status() == 0
+
+
+def test_numbers_past_32_bits_are_refused():
+    q, kp, vp, table, cu, kv = paged_inputs([2], [40], 4, 2, 64, 16, torch.float16, 1, DEV)
+    for most in (2 ** 31, 2 ** 32 + 2, -2 ** 40):
+        with pytest.raises(ValueError, match="max_q_len"):
+            g.gqa_paged_attn(q, kp, vp, table, cu, kv, 0.1, most)
+    with pytest.raises(ValueError):
+        g.paged_build_tables(kv, kv, ints([0]), ints([0]), table, 4, page_size=2 ** 32 + 16)
+    with pytest.raises(ValueError):
+        g.make_paged_dims(1, 4, 2, 64, 16, 2 ** 32 + 4, 3, 2)

@@ -120,3 +120,9 @@ def test_head_counts_are_limited(q, kv, status):
     d = dims(num_q_heads=q, num_kv_heads=kv, num_pages=1, page_size=8, max_tokens=1)
     assert append(L=g.lib(), d=d, q=None, sq=1 << 40, sk=1 << 40, sv=1 << 40) == status
     assert attn(g.lib(), d, q=None) == status
+
+
+def test_numbers_past_32_bits_are_refused():
+    for kw in (dict(num_pages=2 ** 32 + 4), dict(max_tokens=2 ** 31), dict(page_size=2 ** 32 + 16), dict(max_len=-2 ** 31 - 1)):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            dims(**kw)
