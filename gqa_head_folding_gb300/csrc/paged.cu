@@ -12,7 +12,10 @@ namespace {
 
 constexpr int kTabThreads = 1024;
 
+// Every thread of the cluster comes here; .aligned wants a warp's threads together, which after loops of unlike length
+// only __syncwarp promises.
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
