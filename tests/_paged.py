@@ -169,3 +169,66 @@ def paged_inputs(q_lens, kv_lens, Hq, Hkv, D, S, dtype, seed, device, extra=3, w
     cu = torch.tensor([gap + sum(q_lens[:i]) for i in range(len(q_lens) + 1)], dtype=torch.int32, device=device)
     kv = torch.tensor(kv_lens, dtype=torch.int32, device=device)
     return q, kp, vp, table, cu, kv
+
+
+# ---------------------------------------------------------------------------
+# Long contexts: inputs whose outputs show the loss of a key
+# ---------------------------------------------------------------------------
+def counting_ref(seen, heads, G, D):
+    """Share of the first seen[t] tokens whose block of eight is channel d's for head h: token j's is (j // 8 + h / G) % D."""
+    n, h = seen.double()[:, None, None], torch.arange(heads, device=seen.device)[None, :, None] // G
+    e = (torch.arange(D, device=seen.device)[None, None, :] - h) % D
+    whole = torch.div(n, 8 * D, rounding_mode="floor")
+    return (whole * 8 + (n - whole * 8 * D - 8 * e).clamp(0, 8)) / n
+
+
+def even_tolerance(ref, dtype):
+    """Keys that weigh alike: each P is a power of two in the dtype, so only the sums and weights are off, all of one
+    sign: an exponential and two merges (each 2^-22), a division, and sums that are at most 600 additions deep (the tiles
+    of one CTA's range, the steps of a tile, warps, parts): 600 * 2^-24 < 2^-14 in all, and one rounding to the dtype."""
+    return ref * (half_step(dtype) + 2.0 ** -14)
+
+
+def _own_rows(q_lens, kv_lens, device):
+    """For the token in each row of the step: its request, and the tokens it sees."""
+    b = torch.cat([torch.full((n,), i, device=device) for i, n in enumerate(q_lens)])
+    seen = torch.cat([torch.arange(L - n + 1, L + 1, device=device) for n, L in zip(q_lens, kv_lens)])
+    return b, seen
+
+
+def counting_case(q_lens, kv_lens, Hq, Hkv, D, S, dtype, seed, device):
+    """q = 0, so every key weighs the same, and the values count keys: one that is lost, doubled or taken from
+    another place moves a channel by 1 / (kv_len / D) of its value."""
+    q, kp, vp, table, cu, kv = paged_inputs(q_lens, kv_lens, Hq, Hkv, D, S, dtype, seed, device)
+    q.zero_()
+    for b, L in enumerate(kv_lens):
+        j, h = torch.arange(L, device=device)[:, None], torch.arange(Hkv, device=device)[None, :]
+        one = torch.zeros(L, Hkv, D, dtype=dtype, device=device).scatter_(2, ((j // 8 + h) % D)[..., None], 1.0)
+        vp[table[b, j // S].long(), h, j % S] = one
+    ref = counting_ref(_own_rows(q_lens, kv_lens, device)[1], Hq, Hq // Hkv, D)
+    return q, kp, vp, table, cu, kv, ref, even_tolerance(ref, dtype)
+
+
+def dominant_case(q_lens, kv_lens, Hq, Hkv, D, S, dtype, seed, device):
+    """Up to D keys per request and KV head, one in each stretch of the context, outweigh all others (e^-32 each), and
+    each has a channel of its own: one that is not found leaves a channel at 0."""
+    q, kp, vp, table, cu, kv = paged_inputs(q_lens, kv_lens, Hq, Hkv, D, S, dtype, seed, device)
+    q.fill_(1.0)
+    gen = torch.Generator(device=device).manual_seed(seed + 100)
+    own, seen = _own_rows(q_lens, kv_lens, device)
+    ref = torch.zeros(*q.shape, dtype=torch.float64, device=device)
+    h = torch.arange(Hkv, device=device)[:, None]
+    for b, L in enumerate(kv_lens):
+        j = torch.arange(L, device=device)[:, None]
+        kp[table[b, j // S].long(), h.T, j % S] = 0.0
+        n = min(D, L)
+        edge = torch.arange(n + 1, device=device) * L // n
+        at = edge[:-1] + (torch.rand(Hkv, n, generator=gen, device=device) * (edge[1:] - edge[:-1])).long().minimum(edge[1:] - edge[:-1] - 1)
+        page = table[b, at // S].long()
+        kp[page, h, at % S] = 1.0
+        vp[page, h, at % S] = torch.eye(D, dtype=dtype, device=device)[:n].expand(Hkv, n, D)
+        rows = own == b
+        found = (at[None] < seen[rows][:, None, None]).double()  # [row, KV head, key]
+        ref[rows, :, :n] = (found / found.sum(-1, keepdim=True)).repeat_interleave(Hq // Hkv, dim=1)
+    tol = even_tolerance(ref, dtype) + max(kv_lens) * 2.0 ** -46 * 8  # the other keys: e^-32 < 2^-46, |v| < 8
+    return q, kp, vp, table, cu, kv, 32.0 / D, ref, tol

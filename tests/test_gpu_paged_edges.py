@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import gqa_head_folding_gb300 as g
-from _paged import DTYPES, angles, pages_of, paged_inputs, ref_attn, ref_release
+from _paged import DTYPES, angles, counting_case, dominant_case, pages_of, paged_inputs, ref_attn, ref_release
 from gqa_head_folding_gb300.paged import PagedCache
 from test_gpu_paged import append_case
 from test_gpu_paged_run import Loop
@@ -436,3 +436,34 @@ def test_numbers_past_32_bits_are_refused():
         g.paged_build_tables(kv, kv, ints([0]), ints([0]), table, 4, page_size=2 ** 32 + 16)
     with pytest.raises(ValueError):
         g.make_paged_dims(1, 4, 2, 64, 16, 2 ** 32 + 4, 3, 2)
+
+
+# ---------------------------------------------------------------------------
+# Long contexts: outputs that show the loss of a key, a page, a tile or a part
+# ---------------------------------------------------------------------------
+LONG = [([1], [39990], 2), ([1, 1, 1], [39990, 17, 20001], 4), ([4], [39990], 2), ([5], [30001], 2), ([70], [39990], 1), ([300, 1], [20000, 9001], 1)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("S, D", [(16, 64), (128, 128)])
+@pytest.mark.parametrize("q_lens, kv_lens, G", LONG)
+def test_attn_long_contexts_count_their_keys(q_lens, kv_lens, G, S, D, dtype):
+    q, kp, vp, table, cu, kv, ref, tol = counting_case(q_lens, kv_lens, 8 * G, 8, D, S, DTYPES[dtype], 3, DEV)
+    out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, D ** -0.5, max(q_lens))
+    torch.cuda.synchronize()
+    assert g.device_status() == 0
+    err = (out.double() - ref).abs()
+    assert (err <= tol).all(), f"max err {err.max():.3e}, {(err / tol.clamp(min=1e-30)).max():.2f} of its bound"
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("S, D", [(16, 64), (64, 128)])
+@pytest.mark.parametrize("q_lens, kv_lens, G", LONG)
+def test_attn_long_contexts_find_their_keys(q_lens, kv_lens, G, S, D, dtype):
+    for seed in range(3):
+        q, kp, vp, table, cu, kv, scale, ref, tol = dominant_case(q_lens, kv_lens, 8 * G, 8, D, S, DTYPES[dtype], seed, DEV)
+        out = g.gqa_paged_attn(q, kp, vp, table, cu, kv, scale, max(q_lens))
+        torch.cuda.synchronize()
+        assert g.device_status() == 0
+        err = (out.double() - ref).abs()
+        assert (err <= tol).all(), f"max err {err.max():.3e}, {(err / tol.clamp(min=1e-30)).max():.2f} of its bound"

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gqa_head_folding_gb300 as g
+from _paged import counting_case, counting_ref, dominant_case, even_tolerance, ref_attn
 
 FAKE = ctypes.c_void_p(0x10000)   # aligned, never dereferenced
 OTHER = ctypes.c_void_p(0x20000)
@@ -126,3 +127,29 @@ def test_numbers_past_32_bits_are_refused():
     for kw in (dict(num_pages=2 ** 32 + 4), dict(max_tokens=2 ** 31), dict(page_size=2 ** 32 + 16), dict(max_len=-2 ** 31 - 1)):
         with pytest.raises(ValueError, match=next(iter(kw))):
             dims(**kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_context_bound_sees_a_lost_page(dtype, D):
+    """Leaving out (or counting twice) any page of 40,000 tokens moves an output of the counting case past its bound, a page of
+    eight as well as a tile of 128; in fp16 a single key does."""
+    L, heads = 39990, 2
+    ref = counting_ref(torch.tensor([L]), heads, 1, D)[0]
+    tol = even_tolerance(ref, dtype)
+    for size in (8, 16, 128) + ((1,) if dtype == torch.float16 else ()):
+        first = torch.arange(1, L, size)
+        upto = lambda n: counting_ref(n, heads, 1, D) * n[:, None, None]  # noqa: E731
+        lost = upto((first + size).clamp(max=L)) - upto(first)
+        n = lost.sum(-1, keepdim=True)
+        for wrong in ((ref * L - lost) / (L - n), (ref * L + lost) / (L + n)):
+            assert ((wrong - ref).abs() > tol).any(-1).all()
+
+
+def test_long_context_cases_agree_with_the_definition():
+    for case in (counting_case, dominant_case):
+        for dtype in (torch.float16, torch.bfloat16):
+            args = ([1, 5, 40], [700, 23, 301], 4, 2, 64, 16, dtype, 3, "cpu")
+            q, kp, vp, table, cu, kv, *scale, ref, tol = case(*args)
+            want, _ = ref_attn(q, kp, vp, table, cu.tolist(), kv.tolist(), scale[0] if scale else 0.125, torch.zeros_like(q))
+            assert ((want - ref).abs() <= tol).all() and bool((ref.sum(-1) - 1).abs().max() < 1e-9)
