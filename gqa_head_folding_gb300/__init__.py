@@ -698,8 +698,13 @@ def paged_workspace_bytes(dims: PagedDims) -> int:
 
 
 def alloc_paged_workspace(dims: PagedDims, device) -> torch.Tensor:
-    """Workspace for gqa_paged_attn, its counters zero (they stay so between calls; what follows them holds anything).
+    """Zero-filled workspace for gqa_paged_attn (its counters stay zero between calls).
     Its size depends on head_dim and the device only, so one serves every batch and every layer in a stream."""
+    return torch.zeros(paged_workspace_bytes(dims), dtype=torch.uint8, device=device)
+
+
+def _paged_workspace_of_one_call(dims: PagedDims, device) -> torch.Tensor:
+    """A workspace with zeros where the library needs them: filling all 40 MB would take longer than many calls."""
     workspace = torch.empty(paged_workspace_bytes(dims), dtype=torch.uint8, device=device)
     workspace[:GQAQ_PAGED_COUNTER_BYTES].zero_()
     return workspace
@@ -892,7 +897,7 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, cu_q, kv_len, scale: float,
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = alloc_paged_workspace(dims.contents, q.device)
+        workspace = _paged_workspace_of_one_call(dims.contents, q.device)
     (nbytes,) = _paged_dim("workspace", workspace, 1)
     status = lib().gqa_paged_attn(
         dims, _int32("max_q_len", max_q_len), aq, _paged("k_pages", k_pages, dt, pool, dev),
