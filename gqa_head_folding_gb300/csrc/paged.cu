@@ -282,14 +282,6 @@ __device__ __forceinline__ void unpack8(const uint4 &x, f32x2 (&y)[4]) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const f32x2 (&y)[4]) {
     uint32_t w[4];
 #pragma unroll

@@ -163,14 +163,6 @@ __device__ __forceinline__ void warp_commit(uint32_t bar) {
         : "memory");
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // The softmax warps' place in the CTA's range. One thread moves it on and all
 // read it from shared memory: held by each thread it spilled registers of the
 // loop over tiles, whose reloads missed the small L1 that is left beside the
