@@ -67,7 +67,8 @@ struct TablesParams {
 // shared out over the grid's threads, each finding its request by a binary
 // search of the sums in shared memory. A new page's index follows from the
 // sums and the free list alone, so no thread waits for another's table entry.
-// Latency bounds it: 4.9 us for 32 requests, 6.6 us for 256 requests and 37K rows.
+// Latency bounds it: 4.9 us for 32 requests, 6.6 us for 256 requests and 37K rows (5.0
+// and 9.1 with the count replaced in place, which keeps the grid to eight CTAs).
 __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesParams p) {
     extern __shared__ int sm[];
     int *cu = sm;                // [B + 1] first row of each request, clamped to T
@@ -167,7 +168,7 @@ struct ReleaseParams {
 
 // The same shape as the plan: every CTA sums the pages that
 // leave, then each thread moves some of them (154K pages of 500 requests: 6.6
-// us; 30 us with a single cluster of eight CTAs).
+// us; 31 us in the one cluster of eight CTAs that a count in place takes).
 __global__ void __launch_bounds__(kTabThreads) paged_release_kernel(const ReleaseParams p) {
     extern __shared__ int sm[];
     int *cum = sm;               // [B + 1] leaving pages before each request

@@ -20,10 +20,10 @@
 // range boundary leaves an fp32 partial and the CTA that arrives last merges
 // them.
 //
-// What bounds it: HBM (batch 8 at up to 64K, 8 KV heads of 128 channels: 222 us,
-// 6.66 TB/s, 98% of the copy rate); with little data the chain of schedule (2
+// What bounds it: HBM (batch 8 at up to 64K, 8 KV heads of 128 channels: 224 us,
+// 6.6 TB/s, 97% of the copy rate); with little data the chain of schedule (2
 // us), first tile (1.3), tiles, state merge (0.6), arrival (1.1) and merge of
-// the parts (one request at 4K: 10.3 us).
+// the parts (one request at 4K, 8 KV heads of 64 channels: 10.3 us).
 #include <math.h>
 
 #include <atomic>
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kRows = 8;          // rows of an item: q_len * G at most
 constexpr int kItemTiles = 1;     // what an item costs beside its tiles, in tiles
-constexpr int kMinUnits = 2;      // tiles per CTA below which a small step uses fewer CTAs (four: 11.0 us for 32 KV-head contexts of 4K, two: 9.9)
+constexpr int kMinUnits = 2;      // tiles per CTA below which a small step uses fewer CTAs (8 KV heads of 64 channels over 4K tokens: two 10.4 us, four 11.7)
 
 template <int D>
 struct PdCfg {
@@ -492,8 +492,9 @@ size_t paged_attn_workspace_bytes(const gqaq_paged_dims *d, const LaunchCtx &ctx
 
 int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (a.workspace_bytes < paged_attn_workspace_bytes(a.dims, ctx)) return GQAQ_ERR_WORKSPACE;
-    // Up to eight rows per KV head: the decode kernel (one request at 4K 12.8 us against 20.9, batch 32 at D = 64 32.5
-    // against 49); above, the tensor-memory kernel (12 to 24 rows: 47 to 65 us against 52 to 196 with more N blocks).
+    // Up to eight rows per KV head: the decode kernel (32 query and 8 KV heads of 64 channels: one request at 4K 10.4 us
+    // against 18.4, 32 requests of 1K to 4K 31.4 against 43.8); above, the tensor-memory kernel (16 requests of up to 9K with 3
+    // to 6 drafted tokens, 12 to 24 rows: 44 to 65 us, where two and three N blocks of mma.sync took 52 to 196).
     if ((int64_t)a.max_q_len * (a.dims->num_q_heads / a.dims->num_kv_heads) > kRows) return launch_paged_tc(a, ctx);
     if (a.dims->dtype == GQAQ_BF16) return a.dims->head_dim == 128 ? launch_decode<128, true>(a, ctx) : launch_decode<64, true>(a, ctx);
     return a.dims->head_dim == 128 ? launch_decode<128, false>(a, ctx) : launch_decode<64, false>(a, ctx);

@@ -29,15 +29,17 @@
 //  - an item cut by the end of a range leaves fp32 partials (m, l, acc), laid
 //    out [channel / 4][row] so that a warp's stores are contiguous; the CTA
 //    that arrives last merges them and resets the counter.
-//  - warp 19 watches the S barriers for the softmax warps and clears the rows
-//    of a last page that lie past its request.
+//  - warp 19 watches the S barriers for the softmax warps. These clear the rows
+//    of a last page's V that lie past its request.
 //
-// What bounds it: the tensor core where a chunk is long (1024 tokens at the end
-// of 32K, 32 heads of 128 channels: 404 to 430 us, up to 1,340 TFLOP/s, 71% of
-// the measured GEMM rate in bursts; in long runs the power limit, 66%), HBM
-// where rows are few (five drafted tokens of 16 requests: 34 tiles of 64 KB in
-// 43.5 us on each SM), and the start and end of items where contexts are short
-// (3 to 6 us each).
+// What bounds it. Where a chunk is long (1024 tokens at the end of 32K, 32 heads
+// of 128 channels): in bursts at 2,070 MHz the chain from S over the softmax to
+// PV (420 us, 1,290 TFLOP/s, 68% of the measured GEMM rate; at 8K the tensor
+// pipe is busy 48% of the cycles, the one of the exponentials 24%), in a running
+// stream the power cap (1,370 W, 1,570 MHz: 475 us, 67% of the sustained rate).
+// HBM where rows are few (five drafted tokens of 16 requests, contexts up to 9K,
+// 8 KV heads of 128 channels: 34 tiles of 64 KB in 43.5 of 64 us on each SM),
+// and the start and end of items where contexts are short (3 to 4 us each).
 #include <math.h>
 
 #include "paged_sched.cuh"
