@@ -10,8 +10,8 @@ Requests of unlike lengths share one pool of pages per layer. A step runs
 
 with one plan for all layers: every layer's pools use the same page indices. A planned step is
 committed or released before the next is planned (its pages are otherwise lost to the pool). Everything
-a step reads or writes on the device lies in buffers that this object keeps, so plan, append, attend and
-commit can be captured in a CUDA graph (after one eager step) and replayed with new contents of new_len.
+a step reads or writes on the device lies in buffers that this object keeps, so the five can be captured
+in a CUDA graph (after one eager step) and replayed with new contents of new_len and keep_len.
 
 This module only sequences library calls and owns the buffers they share.
 """

@@ -107,6 +107,47 @@ def test_release_of_a_planned_step():
     assert L.c.cache_len.tolist() == [60, 20, 33]
 
 
+def test_drafting_step_captured_with_its_release():
+    """A step of drafted tokens and the release of the rejected ones in one graph, replayed with other lengths, one of them refused."""
+    caches = [PagedCache(1, 3, 4, 2, 64, 30, 100, 20, DEV) for _ in range(2)]
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.zeros(15, 8, 64, dtype=torch.float16, device=DEV)
+    q, k, v = x.split([4, 2, 2], dim=1)
+    new, keep = (torch.zeros(3, dtype=torch.int32, device=DEV) for _ in range(2))
+    outs = [torch.zeros(15, 4, 64, dtype=torch.float16, device=DEV) for _ in range(2)]
+    q_out = torch.zeros_like(outs[0])
+
+    def step(i):
+        c = caches[i]
+        c.plan(new, 15)
+        c.attend(0, c.append(0, q, k, v, q_out=q_out), 5, outs[i])
+        c.commit()
+        c.release(keep)
+
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        step(0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            step(0)
+    lens = [0, 0, 0]
+    for n, k_ in (([5, 5, 5], [4, 5, 2]), ([5, 1, 5], [9, 3, 99]), ([0, 5, 5], [0, 8, -1]), ([5, 5, 5], [5, 13, 15])):
+        x.copy_(torch.randn(x.shape, generator=gen, device=DEV))
+        new.copy_(ints(n))
+        keep.copy_(ints(k_))
+        torch.cuda.synchronize()
+        g.device_status()
+        graph.replay()
+        torch.cuda.synchronize()
+        step(1)
+        torch.cuda.synchronize()
+        lens = [w if 0 <= w <= a + b else a + b for a, b, w in zip(lens, n, k_)]
+        assert g.device_status() == (g.GQAQ_DEV_BAD_LEN if 99 in k_ or -1 in k_ else 0)
+        assert torch.equal(*outs) and caches[0].cache_len.tolist() == lens
+        for name in ("cache_len", "kv_len", "block_table", "free_count", "free_pages"):
+            assert torch.equal(*(getattr(c, name) for c in caches)), name
+
+
 # ---------------------------------------------------------------------------
 # NaN and infinity in live rows
 # ---------------------------------------------------------------------------
