@@ -225,10 +225,15 @@ struct PagedWarp {
 // of the codes, ke and ve their pages' exponents and s = scale log2(e) 2^ke q . code_k:
 //   w = 2^(s + ve - ref),  O += w code_v,  l += w 2^-ve,  out = O / l
 // so neither exponent meets a number of 16 bits, and the codes reach the tensor
-// core as they decode, exactly, to fp16. Queries are fp16 there too: a bfloat16
-// row is taken times a power of two that brings its largest channel under 2^15
-// (a channel 2^-38 of that and less loses bits, 2^-40 of the score's terms),
-// and P, rounded once to fp16, is finer than bfloat16 would be.
+// core as they decode, exactly, to fp16. The largest w is at least 2^kHeadroom;
+// a tile with a page more than kHeadroom exponents under the item's largest so
+// far takes its w in two bfloat16 numbers (the loader marks it: the factors of its
+// keys are negative): the batch of 8 at 64K takes 149 us for 132 where every
+// context begins with such a large page. A tile's whole work in two copies costs
+// nothing where there is none; one copy with a branch before V took 147. Queries
+// are fp16 there too: a bfloat16 row is taken times a power of two that brings its
+// largest channel under 2^15 (a channel 2^-38 of that and less loses bits, 2^-40
+// of the score's terms).
 // Lane r * 4 + c reads bytes D/4 c .. of K rows r and r + 8, and bytes D/8 r ..
 // of V rows 2c, 2c + 1, 2c + 8 and 2c + 9: channel (D/4) c + 4 j + e of q meets
 // its like in step j, and channel (D/8) r + 2 i + h of O lies in o[i][2 h], o[i][2 h + 1].
@@ -302,6 +307,11 @@ struct PagedWarp8 {
     // As PagedWarp::tile; f0, f1: factors of the pages of this lane's tokens r and r + 8. A code is decoded once for
     // all NB blocks of eight rows.
     __device__ __forceinline__ void tile(uint32_t kb, uint32_t vb, int row0, int tok0, int n, bool mask, const float2 &f0, const float2 &f1) {
+        if (__builtin_expect(__any_sync(0xffffffffu, f0.x < 0.f), 0)) tile_of<true>(kb, vb, row0, tok0, n, mask, f0, f1);
+        else tile_of<false>(kb, vb, row0, tok0, n, mask, f0, f1);
+    }
+    template <bool FAR>
+    __device__ __forceinline__ void tile_of(uint32_t kb, uint32_t vb, int row0, int tok0, int n, bool mask, const float2 &f0, const float2 &f1) {
         constexpr int KB = D / 4, VB = D / 8;  // bytes of a row that a lane reads
         float s[NB][4];
         {
@@ -335,7 +345,7 @@ struct PagedWarp8 {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 &f = e < 2 ? f0 : f1;
-                s[b][e] = fmaf(s[b][e] * f.x, mul[b][e & 1], f.y);
+                s[b][e] = fmaf(s[b][e] * (FAR ? fabsf(f.x) : f.x), mul[b][e & 1], f.y);
             }
         if (mask) {
 #pragma unroll
@@ -379,7 +389,7 @@ struct PagedWarp8 {
         uint32_t pb[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const float r0 = m[b][0] == -INFINITY ? 0.f : m[b][0], r1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+            const float r0 = m[b][0] == -INFINITY ? 0.f : m[b][0] - kHeadroom, r1 = m[b][1] == -INFINITY ? 0.f : m[b][1] - kHeadroom;
             s[b][0] = fast_exp2(s[b][0] - r0);
             s[b][1] = fast_exp2(s[b][1] - r1);
             s[b][2] = fast_exp2(s[b][2] - r0);
@@ -387,6 +397,9 @@ struct PagedWarp8 {
             l[b][0] = fmaf(s[b][0], u0, fmaf(s[b][2], u1, l[b][0]));
             l[b][1] = fmaf(s[b][1], u0, fmaf(s[b][3], u1, l[b][1]));
         }
+        const bool cut = n < 16;  // rows behind the request may hold anything: 0 * NaN would reach O
+        const uint32_t mk0 = (2 * c < n ? 0x0000ffffu : 0u) | (2 * c + 1 < n ? 0xffff0000u : 0u);
+        const uint32_t mk1 = (2 * c + 8 < n ? 0x0000ffffu : 0u) | (2 * c + 9 < n ? 0xffff0000u : 0u);
         uint32_t v[4][VB / 4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -399,14 +412,15 @@ struct PagedWarp8 {
                 v[t][0] = x.x; v[t][1] = x.y;
             }
         }
+        if constexpr (FAR) {
+            far_values(s, vb, row0, cut, mk0, mk1);
+            return;
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             pb[b][0] = movmatrix_trans(pack2<false>(s[b][0], s[b][1]));
             pb[b][1] = movmatrix_trans(pack2<false>(s[b][2], s[b][3]));
         }
-        const bool cut = n < 16;  // rows behind the request may hold anything: 0 * NaN would reach O
-        const uint32_t mk0 = (2 * c < n ? 0x0000ffffu : 0u) | (2 * c + 1 < n ? 0xffff0000u : 0u);
-        const uint32_t mk1 = (2 * c + 8 < n ? 0x0000ffffu : 0u) | (2 * c + 9 < n ? 0xffff0000u : 0u);
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // channels 2i, 2i + 1 of two tokens, token inner
@@ -421,6 +435,36 @@ struct PagedWarp8 {
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) mma_16816(o[b][i], a, pb[b][0], pb[b][1]);
+        }
+    }
+    // O += w code_v of 16 tokens whose page lies far under another: w in two bfloat16 numbers, which have 32-bit floats' range.
+    // One block of rows after the other, so that the two need no registers that the common way does not have.
+    __device__ __forceinline__ void far_values(const float (&s)[NB][4], uint32_t vb, int row0, bool cut, uint32_t mk0, uint32_t mk1) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t x = pack2<true>(s[b][2 * h], s[b][2 * h + 1]);
+                hi[h] = movmatrix_trans(x);
+                lo[h] = movmatrix_trans(pack2<true>(s[b][2 * h] - __uint_as_float(x << 16), s[b][2 * h + 1] - __uint_as_float(x & 0xffff0000u)));
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+                uint32_t a[4], y[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t] = lds32(at(vb, row0 + 2 * c + (t & 1) + (t >> 1) * 8, (D / 8) * r + 4 * (i >> 1)));
+                e4m3x4_to_f16x2x2(byte_perm(y[0], y[1], sel), a[0], a[1]);
+                e4m3x4_to_f16x2x2(byte_perm(y[2], y[3], sel), a[2], a[3]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    a[x] = f16x2_to_bf16x2(a[x]);
+                    if (cut) a[x] &= x < 2 ? mk0 : mk1;
+                }
+                mma16<true>(o[b][i], a, hi[0], hi[1]);
+                mma16<true>(o[b][i], a, lo[0], lo[1]);
+            }
         }
     }
     // (m, l, acc) of rows first .. first + MROWS - 1, which are of block b, to this warp's slot of the merge buffer.
@@ -523,7 +567,7 @@ __device__ __forceinline__ void paged_decode(const CUtensorMap &kmap, const CUte
                         const uint32_t dst = smem_u32(stages + s * C::STAGE) + (uint32_t)lane * box;
                         tma_load_2d(dst, &kmap, 0, row, fb, pol);
                         tma_load_2d(dst + C::KBYTES, &vmap, 0, row, fb, pol);
-                        factors[s * 16 + lane] = page_factors2(ke, ve);
+                        factors[s * 16 + lane] = page_factors2(ke, ve, feed.far);
                     }
                     __syncwarp();  // the factors are written before the phase can end
                     if (lane == 0) mbar_arrive(fb);

@@ -7,12 +7,18 @@
 //   s = scale log2(e) 2^ke (q . code_k) + ve,   w = 2^(s - ref)
 //   O += w code_v,   l += w 2^-ve,   out = O / l
 // Neither exponent meets a number of 16 bits: the codes become fp16 exactly as
-// they are, and w, rounded once to fp16, is relative to the row's largest weight
-// times 2^ve. The products are fp16 whatever the dtype: a bfloat16 row of q is
-// taken times a power of two that brings its largest channel under 2^15 (a
-// channel 2^-38 of that and less loses bits, 2^-40 of the score's terms), since
-// both operands of a product have one type and a code costs a conversion more
-// to bfloat16. The reference moves as in paged_attn_tc.cu.
+// they are, and w is rounded once to fp16, or taken in two bfloat16 numbers, and
+// the codes in bfloat16, where a segment's pages of V lie more than kHeadroom
+// exponents apart. The walker looks through their exponents while the segment's
+// first tiles are on their way. P of 16 tokens is then eight columns of the first
+// numbers and eight of the second, in place of the 16 scores: the 1024-token chunk
+// below takes 944 us for 441 where every segment has such pages. Each role's loop in
+// two copies costs 3 us there; a flag per tile, read in one loop, took 502 to 532.
+// The products of scores are fp16 whatever the dtype: a bfloat16 row of q is taken
+// times a power of two that brings its largest channel under 2^15 (a channel 2^-38
+// of that and less loses bits, 2^-40 of the score's terms), since both operands of
+// a product have one type and a code costs a conversion more to bfloat16. The
+// reference moves as in paged_attn_tc.cu.
 //
 // Kernel shape: that of paged_attn_tc.cu (items of 256 rows, two softmax groups
 // with S and O in tensor memory, the notifier, the same end of an item), with
@@ -27,7 +33,7 @@
 //    the softmax warps have no room to give (they hold 96, the others 48).
 //
 // What bounds it. A 1024-token chunk of a 32K context (32 heads of 128 channels):
-// 437 us, 1,240 TFLOP/s, 63% of a large library product's rate; the tensor pipe is busy 53% of
+// 441 us, 1,230 TFLOP/s, 63% of a large library product's rate; the tensor pipe is busy 53% of
 // the cycles and the exponentials 26%, and the rest is the chain S, softmax, PV of
 // the two row tiles. Sixteen requests of up to 9K tokens with seven drafted tokens
 // (28 live rows of 128; 8 KV heads of 128 channels): 69 us for 25 us of bytes.
@@ -54,9 +60,9 @@ struct P8Cfg : PtcShape<D> {
     // tile NR1 before it is free, so that V of tile t - NR1 / 2 - 1 has been widened, for which PV of tile
     // t - NR1 / 2 - 1 - NV, and with it that tile's softmax, had ended.
     static constexpr int NF = NR1 / 2 + 1 + NV;
-    static constexpr int NSEG = 4;
+    static constexpr int NSEG = 3;
     static constexpr int SEG = 8 * ((int)(sizeof(PagedWalk) + 7) / 8 + 1);
-    static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR1 + NF + 2 * NSEG + 11;
+    static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR1 + NF + 3 * NSEG + 11;
     // bytes from the start of shared memory: two Q tiles, the raw ring, the K and V rings, the exchange of 256 numbers, the
     // factors, the barriers, and what the schedule and the walker leave
     static constexpr int AT_R = 2 * PtcShape<D>::TILE, AT_K = AT_R + NR * RAW, AT_V = AT_K + NK * PtcShape<D>::TILE;
@@ -67,7 +73,7 @@ struct P8Cfg : PtcShape<D> {
     // the barriers
     static constexpr int KFULL = AT_BAR, KEMPTY = KFULL + 8 * NK, VFULL = KEMPTY + 8 * NK, VEMPTY = VFULL + 8 * NV;
     static constexpr int RFULL = VEMPTY + 8 * NV, REMPTY = RFULL + 8 * NR1, FFULL = REMPTY + 8 * NR1, SEG_FULL = FFULL + 8 * NF;
-    static constexpr int SEG_EMPTY = SEG_FULL + 8 * NSEG, QFULL = SEG_EMPTY + 8 * NSEG, QEMPTY = QFULL + 8;
+    static constexpr int SEG_EMPTY = SEG_FULL + 8 * NSEG, FAR_FULL = SEG_EMPTY + 8 * NSEG, QFULL = FAR_FULL + 8 * NSEG, QEMPTY = QFULL + 8;
     static constexpr int QREADY = QEMPTY + 8;    // Q has been turned into fp16 (bfloat16 only)
     static constexpr int S_READY = QREADY + 8, P_READY = S_READY + 16;
     static constexpr int O_DONE = P_READY + 16;  // a group's last PV of a segment
@@ -76,6 +82,8 @@ struct P8Cfg : PtcShape<D> {
     static_assert((NR1 - NR) * RAW <= PtcShape<D>::TILE, "the second row tile's place");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+static_assert(kRefDrop >= kHeadroom, "the largest weight of a row");
 
 struct P8Params : PtcParams {
     const int8_t *k_exp, *v_exp;
@@ -86,6 +94,7 @@ template <int D>
 struct P8Segment {
     PagedWalk w;
     int more;  // 0: the range is done
+    int far;   // known later (FAR_FULL): its weights are bfloat16 numbers
 };
 
 // 128 rows of D codes, brought by TMA (D = 128: 128-byte swizzled, D = 64: as
@@ -137,7 +146,66 @@ __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t dst, int warp,
     }
 }
 
+// What this thread has just widened (its zeros too), fp16 to bfloat16 in place.
+template <int D>
+__device__ __forceinline__ void rewiden_tile(uint32_t dst, int warp, int lane) {
+    const int c = lane & 3, r8 = D == 128 ? (lane >> 3) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+    const uint32_t to = dst + (uint32_t)((warp * 32 + r8) * 128 + (((2 * c) ^ r8) << 4));
+#pragma unroll 1
+    for (int k = 0; k < 2 * (D / 16); ++k) {
+        const int step = k >> 1, kh = D == 128 ? step & 1 : 0, g = D == 128 ? step >> 1 : step;
+        const uint32_t at = (to ^ (uint32_t)((k & 1) << 4)) + (uint32_t)(kh * PtcShape<D>::BLK + g * 1024);
+        const uint4 x = lds128(at);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f16x2_to_bf16x2(x.x)), "r"(f16x2_to_bf16x2(x.y)),
+                     "r"(f16x2_to_bf16x2(x.z)), "r"(f16x2_to_bf16x2(x.w))
+                     : "memory");
+    }
+}
+
+// The product of 32 tokens' weights in two bfloat16 numbers: of each 16 tokens A has eight columns of the first and eight of the
+// second; B as warp_mma_ts4.
+__device__ __forceinline__ void warp_mma_far(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred q, p, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s64 b1, %2, 128;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Whether a segment's weights have to be bfloat16 numbers: it has pages of V more than kHeadroom exponents apart. For a
+// warp: 256 pages at a time, whose exponents are on their way while the next ones' table entries are (8 K tokens in pages of 16
+// take about 1.5 us, beside the segment's first loads).
+__device__ __forceinline__ bool segment_far(const P8Params &p, const PagedWalk &w, int lane) {
+    const int log = kPagedTileLog - p.w.shift, held = (int)(((int64_t)w.s.len + (1 << p.w.shift) - 1) >> p.w.shift);
+    const int *table = p.w.table + (int64_t)w.b * p.w.max_pages;
+    const int last = min((w.local + w.seg_len()) << log, held);
+    int lo = kMostPageExp, hi = kLeastPageExp, page[8];
+    auto entries = [&](int e0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) page[u] = e0 + 32 * u < last ? table[e0 + 32 * u] : -1;
+    };
+    entries((w.local << log) + lane);
+    for (int e0 = (w.local << log) + lane; e0 - lane < last; e0 += 256) {
+        int e[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) e[u] = (uint32_t)page[u] < (uint32_t)p.w.num_pages ? p.v_exp[page[u] * p.w.Hkv + w.kv] : 0;  // a bad page: zeros
+        entries(e0 + 256);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int x = min(max(e[u], kLeastPageExp), kMostPageExp);
+            lo = e0 + 32 * u < last ? min(lo, x) : lo;
+            hi = e0 + 32 * u < last ? max(hi, x) : hi;
+        }
+    }
+    return __reduce_max_sync(0xffffffffu, hi) - __reduce_min_sync(0xffffffffu, lo) > (int)kHeadroom;
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
@@ -164,6 +232,7 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
         init(C::REMPTY, C::NR1, 4);
         init(C::FFULL, C::NF, 1);
         init(C::SEG_FULL, C::NSEG, 1);
+        init(C::FAR_FULL, C::NSEG, 1);
         init(C::SEG_EMPTY, C::NSEG, 8);  // loader, MMA, notifier, four widening warps, softmax
         init(C::QFULL, 3, 1);            // and QEMPTY, QREADY
         init(C::S_READY, 2, 1);
@@ -201,6 +270,9 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
             return mbar_wait(at + C::SEG_FULL + 8 * (i % C::NSEG), (uint32_t)(i / C::NSEG) & 1u, seg_ns, nullptr) && segment(i).more != 0;
         };
         auto seg_next = [&](int i) { return __all_sync(0xffffffffu, seg_wait(i)) != 0; };  // a warp
+        auto seg_far = [&](int i) {  // a thread
+            return mbar_wait(at + C::FAR_FULL + 8 * (i % C::NSEG), (uint32_t)(i / C::NSEG) & 1u, seg_ns, nullptr) && segment(i).far != 0;
+        };
         auto seg_done = [&](int i) { mbar_arrive(at + C::SEG_EMPTY + 8 * (i % C::NSEG)); };
 
         if (warp >= 16) {
@@ -208,21 +280,28 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
             if (warp == 18) {
                 // ---- walker ----
-                if (lane == 0) {
-                    PagedWalk w;
-                    bool more = w.init(p.w, *sched);
-                    for (int i = 0;; ++i) {
-                        if (i >= C::NSEG && !mbar_wait(at + C::SEG_EMPTY + 8 * (i % C::NSEG), ((uint32_t)(i / C::NSEG) & 1u) ^ 1u, seg_ns, nullptr)) {
-                            fail();
-                            break;
-                        }
-                        P8Segment<D> &s = segment(i);
+                PagedWalk w;
+                bool more = w.init(p.w, *sched);
+                for (int i = 0;; ++i) {
+                    bool ok = true;
+                    if (i >= C::NSEG) ok = lane != 0 || mbar_wait(at + C::SEG_EMPTY + 8 * (i % C::NSEG), ((uint32_t)(i / C::NSEG) & 1u) ^ 1u, seg_ns, nullptr);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) fail();
+                        break;
+                    }
+                    P8Segment<D> &s = segment(i);
+                    if (lane == 0) {
                         s.w = w;
                         s.more = more;
                         mbar_arrive(at + C::SEG_FULL + 8 * (i % C::NSEG));
-                        if (!more) break;
-                        more = w.advance(p.w);
                     }
+                    if (!more) break;
+                    const bool far = segment_far(p, w, lane);
+                    if (lane == 0) {
+                        s.far = far;
+                        mbar_arrive(at + C::FAR_FULL + 8 * (i % C::NSEG));
+                    }
+                    more = w.advance(p.w);
                 }
                 __syncwarp();
             } else if (warp == 16) {
@@ -300,7 +379,7 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
             } else if (warp == 17) {
                 // ---- MMA issuer: as in paged_attn_tc.cu, over the widened tiles ----
                 constexpr uint32_t IDESC_S = umma_idesc(128, 128, 0);
-                constexpr uint32_t IDESC_O = umma_idesc(128, D, 1);
+                constexpr uint32_t IDESC_O = umma_idesc(128, D, 1), IDESC_FAR = umma_idesc(128, D, 1, 1);
                 const uint64_t qdesc0 = umma_desc(at, 16);
                 const uint64_t kdesc0 = umma_desc(at + C::AT_K, 16);
                 const uint64_t vdesc0 = umma_desc(at + C::AT_V, C::BLK);
@@ -312,7 +391,7 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     return warp_mbar_wait(bar, parity, p.timeout_ns, abort_flag);
                 };
-                auto products = [&](auto dual_c, int ne, bool first_seg) {
+                auto products = [&](auto dual_c, int sg, int ne) {
                     constexpr bool DUAL = decltype(dual_c)::value;
                     auto issue_s = [&](int e) {
                         const int x = e & 1;
@@ -337,29 +416,39 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
                     };
                     issue_s(0);
                     if (ok && ne > 1) issue_s(1);
+                    auto pv = [&](auto far_c) {
 #pragma unroll 1
-                    for (int e = 0; e < ne && ok; ++e) {
-                        const int x = e & 1;
-                        if (!DUAL || x == 0) ok = wait(at + C::VFULL + 8 * vs, vp);
-                        if (e == 0 && !first_seg) ok = ok && wait(at + C::O_FREE, sp ^ 1u);  // the last segment's O has been read
-                        ok = ok && wait(at + C::P_READY + 8 * x, (pp >> x) & 1u);
-                        if (!ok) break;
-                        pp ^= 1u << x;
-                        tc_fence_after();
-                        const uint64_t vd = vdesc0 + (uint64_t)(vs * (C::TILE >> 4));
-                        const uint32_t od = tbase + C::O_COL + 128u * (uint32_t)x, pd = tbase + C::S_COL + 128u * (uint32_t)x;
-                        warp_mma_ts4(od, pd, vd, IDESC_O, e > 1);              // P of tokens 0-63: columns 0-31
-                        warp_mma_ts4(od, pd + 64u, vd + 512u, IDESC_O, 1);     // of tokens 64-127: columns 64-95
-                        if (!DUAL || x == 1) {
-                            warp_commit(at + C::VEMPTY + 8 * vs);
-                            if (++vs == C::NV) {
-                                vs = 0;
-                                vp ^= 1u;
+                        for (int e = 0; e < ne && ok; ++e) {
+                            const int x = e & 1;
+                            if (!DUAL || x == 0) ok = wait(at + C::VFULL + 8 * vs, vp);
+                            if (e == 0 && sg > 0) ok = ok && wait(at + C::O_FREE, sp ^ 1u);  // the last segment's O has been read
+                            ok = ok && wait(at + C::P_READY + 8 * x, (pp >> x) & 1u);
+                            if (!ok) break;
+                            pp ^= 1u << x;
+                            tc_fence_after();
+                            const uint64_t vd = vdesc0 + (uint64_t)(vs * (C::TILE >> 4));
+                            const uint32_t od = tbase + C::O_COL + 128u * (uint32_t)x, pd = tbase + C::S_COL + 128u * (uint32_t)x;
+                            if constexpr (decltype(far_c)::value) {
+#pragma unroll
+                                for (uint32_t c = 0; c < 4; ++c)  // of tokens 32 c ..: columns 32 c ..
+                                    warp_mma_far(od, pd + 32u * c, vd + 256u * c, IDESC_FAR, e > 1 || c > 0);
+                            } else {
+                                warp_mma_ts4(od, pd, vd, IDESC_O, e > 1);              // P of tokens 0-63: columns 0-31
+                                warp_mma_ts4(od, pd + 64u, vd + 512u, IDESC_O, 1);     // of tokens 64-127: columns 64-95
                             }
+                            if (!DUAL || x == 1) {
+                                warp_commit(at + C::VEMPTY + 8 * vs);
+                                if (++vs == C::NV) {
+                                    vs = 0;
+                                    vp ^= 1u;
+                                }
+                            }
+                            if (e + 2 >= ne) warp_commit(at + C::O_DONE + 8 * x);
+                            if (e + 2 < ne) issue_s(e + 2);
                         }
-                        if (e + 2 >= ne) warp_commit(at + C::O_DONE + 8 * x);
-                        if (e + 2 < ne) issue_s(e + 2);
-                    }
+                    };
+                    if (__any_sync(0xffffffffu, seg_far(sg))) pv(std::true_type());
+                    else pv(std::false_type());
                 };
                 for (int sg = 0; seg_next(sg); ++sg) {
                     if (ok) {
@@ -367,8 +456,8 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
                         const int n = w.seg_len(), rows = min(TB, w.s.m - w.rb * TB) * p.G;
                         ok = wait(at + (BF16 ? C::QREADY : C::QFULL), sp);
                         if (ok) {
-                            if (rows > 128) products(std::true_type(), 2 * n, sg == 0);
-                            else products(std::false_type(), n, sg == 0);
+                            if (rows > 128) products(std::true_type(), sg, 2 * n);
+                            else products(std::false_type(), sg, n);
                         }
                         if (!ok && lane == 0) fail();
                     }
@@ -422,10 +511,11 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     return warp_mbar_wait_slow(bar, parity, p.timeout_ns, abort_flag);
                 };
-                auto turn = [&](uint32_t ring, int N, int &slot, uint32_t &ph, uint32_t full, uint32_t empty, int rows) {
+                auto turn = [&](bool far, uint32_t ring, int N, int &slot, uint32_t &ph, uint32_t full, uint32_t empty, int rows) {
                     ok = wait(at + C::RFULL + 8 * rs, rp) && wait(empty + 8 * slot, ph);
                     if (!ok) return;
                     widen_tile<D>(at + at_r + (uint32_t)(rs * C::RAW), ring + (uint32_t)(slot * C::TILE), warp - 20, lane, rows);
+                    if (__builtin_expect(far, 0)) rewiden_tile<D>(ring + (uint32_t)(slot * C::TILE), warp - 20, lane);
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
@@ -444,9 +534,10 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
                 for (int sg = 0; seg_next(sg); ++sg) {
                     const PagedWalk &w = segment(sg).w;
                     const int n = w.seg_len(), first = w.local * kPagedTile, len = w.s.len;
+                    const bool far = __any_sync(0xffffffffu, seg_far(sg));
                     for (int t = 0; t < n && ok; ++t) {
-                        turn(at + C::AT_K, C::NK, ks, kp, at + C::KFULL, at + C::KEMPTY, 128);
-                        if (ok) turn(at + C::AT_V, C::NV, vs, vp, at + C::VFULL, at + C::VEMPTY, len - (first + t * kPagedTile));
+                        turn(false, at + C::AT_K, C::NK, ks, kp, at + C::KFULL, at + C::KEMPTY, 128);
+                        if (ok) turn(far, at + C::AT_V, C::NV, vs, vp, at + C::VFULL, at + C::VEMPTY, len - (first + t * kPagedTile));
                         if (!ok && lane == 0) fail();
                     }
                     __syncwarp();
@@ -541,120 +632,144 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
                 float ref = live ? -INFINITY : INFINITY, l = 0.f;
                 int fs = fs0 + (dual ? 0 : g);
                 if (fs >= C::NF) fs -= C::NF;
-                for (int k = 0; k < nx; ++k) {
-                    const int jj = dual ? k : 2 * k + g;  // tile within the segment
-                    named_bar_sync(10 + g, 288);  // S is complete (after a timeout it holds anything)
-                    tc_fence_after();
-                    if (warp_live) {
-                        const bool mask = jj >= masked_from;  // some row of the warp does not see all of these tokens
-                        const float4 *fac = factors + fs * 16 + 8 * h;  // of tokens 8 i .. of this thread's
-                        uint32_t pk[32];
-                        // P of these tokens against reference r; their sum, and the sum of each over 2^ve
-                        auto exps = [&](float r, float &share) {
-                            const float nref = r == -INFINITY ? 0.f : -r;
-                            float sum = 0.f;
-                            share = 0.f;
+                auto tiles = [&](auto far_c) {
+                    for (int k = 0; k < nx; ++k) {
+                        const int jj = dual ? k : 2 * k + g;  // tile within the segment
+                        named_bar_sync(10 + g, 288);  // S is complete (after a timeout it holds anything)
+                        tc_fence_after();
+                        if (warp_live) {
+                            const bool mask = jj >= masked_from;  // some row of the warp does not see all of these tokens
+                            const float4 *fac = factors + fs * 16 + 8 * h;  // of tokens 8 i .. of this thread's
+                            uint32_t pk[32];
+                            // P of these tokens against reference r; their sum, and the sum of each over 2^ve
+                            auto exps = [&](float r, float &share) {
+                                const float nref = r == -INFINITY ? 0.f : -r;
+                                float sum = 0.f;
+                                share = 0.f;
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t x[32];
-                                tmem_ld32_async(scol + 32u * c, x);
-                                tmem_ld32_wait(x);
-                                if (__builtin_expect(mask, 0)) {
-                                    const int seen = limit() - token(jj) - 32 * c;  // the last of these that the row sees
-                                    const uint32_t hide = p.scale_log2 > 0.f ? 0xff800000u : 0x7f800000u;  // its product is -inf
+                                for (int c = 0; c < 2; ++c) {
+                                    uint32_t x[32];
+                                    tmem_ld32_async(scol + 32u * c, x);
+                                    tmem_ld32_wait(x);
+                                    if (__builtin_expect(mask, 0)) {
+                                        const int seen = limit() - token(jj) - 32 * c;  // the last of these that the row sees
+                                        const uint32_t hide = p.scale_log2 > 0.f ? 0xff800000u : 0x7f800000u;  // its product is -inf
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        if (e > seen) x[e] = hide;
-                                }
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float4 f = fac[4 * c + i];
-                                    const float m = mul * f.x, b = f.y + nref;
-                                    const uint64_t m2 = pair32(m, m), b2 = pair32(b, b);
-                                    uint64_t s8 = 0;
-#pragma unroll
-                                    for (int e = 8 * i; e < 8 * i + 8; e += 2) {
-                                        const float2 y = unpair32(fma2(pair32(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), m2, b2));
-                                        const float e0 = fast_exp2(y.x), e1 = fast_exp2(y.y);
-                                        s8 = e == 8 * i ? pair32(e0, e1) : add2(s8, pair32(e0, e1));
-                                        pk[16 * c + (e >> 1)] = pack2<false>(e0, e1);
+                                        for (int e = 0; e < 32; ++e)
+                                            if (e > seen) x[e] = hide;
                                     }
-                                    const float2 t = unpair32(s8);
-                                    sum += t.x + t.y;
-                                    share = fmaf(t.x + t.y, f.z, share);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float4 f = fac[4 * c + i];
+                                        const float m = mul * f.x, b = f.y + nref;
+                                        const uint64_t m2 = pair32(m, m), b2 = pair32(b, b);
+                                        uint64_t s8 = 0;
+#pragma unroll
+                                        for (int e = 8 * i; e < 8 * i + 8; e += 2) {
+                                            const float2 y = unpair32(fma2(pair32(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), m2, b2));
+                                            const float e0 = fast_exp2(y.x), e1 = fast_exp2(y.y);
+                                            s8 = e == 8 * i ? pair32(e0, e1) : add2(s8, pair32(e0, e1));
+                                            pk[16 * c + (e >> 1)] = pack2<false>(e0, e1);
+                                        }
+                                        const float2 t = unpair32(s8);
+                                        sum += t.x + t.y;
+                                        share = fmaf(t.x + t.y, f.z, share);
+                                    }
                                 }
-                            }
-                            return sum;
-                        };
-                        float cs = 0.f, share = 0.f;
-                        const bool fresh = __all_sync(0xffffffffu, fabsf(ref) == INFINITY);  // of both warps: they share ref
-                        // one copy of the exponentials serves both passes: the second, after a
-                        // row's reference has moved, is rare, and code that is jumped over costs fetches
+                                return sum;
+                            };
+                            float cs = 0.f, share = 0.f;
+                            const bool fresh = __all_sync(0xffffffffu, fabsf(ref) == INFINITY);  // of both warps: they share ref
+                            // one copy of the exponentials serves both passes: the second, after a
+                            // row's reference has moved, is rare, and code that is jumped over costs fetches
 #pragma unroll 1
-                        for (int pass = fresh ? 0 : 1;; ++pass) {
-                            if (pass > 0) cs = exps(ref, share);
-                            if (pass > 1) break;
-                            const bool redo = (ref == -INFINITY && limit() >= (w.local + jj) * kPagedTile) || cs > kSumLimit;  // the row's first keys, or far above
-                            if (__builtin_expect(!pair_any(pair_bar, redo), 1)) {
-                                if (pass == 0) {
+                            for (int pass = fresh ? 0 : 1;; ++pass) {
+                                if (pass > 0) cs = exps(ref, share);
+                                if (pass > 1) break;
+                                const bool redo = (ref == -INFINITY && limit() >= (w.local + jj) * kPagedTile) || cs > kSumLimit;  // the row's first keys, or far above
+                                if (__builtin_expect(!pair_any(pair_bar, redo), 1)) {
+                                    if (pass == 0) {
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) pk[e] = 0u;  // every row of the pair is masked in this tile
+                                        for (int e = 0; e < 32; ++e) pk[e] = 0u;  // every row of the pair is masked in this tile
+                                    }
+                                    break;
                                 }
-                                break;
-                            }
-                            // the row's maximum over both halves becomes the reference
-                            float top = -INFINITY;
+                                // the row's maximum over both halves becomes the reference
+                                float top = -INFINITY;
 #pragma unroll 1
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t x[32];
-                                tmem_ld32_async(scol + 32u * c, x);
-                                tmem_ld32_wait(x);
-                                const int seen = limit() - token(jj) - 32 * c;
+                                for (int c = 0; c < 2; ++c) {
+                                    uint32_t x[32];
+                                    tmem_ld32_async(scol + 32u * c, x);
+                                    tmem_ld32_wait(x);
+                                    const int seen = limit() - token(jj) - 32 * c;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float4 f = fac[4 * c + i];
-                                    const float m = mul * f.x;
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float4 f = fac[4 * c + i];
+                                        const float m = mul * f.x;
 #pragma unroll
-                                    for (int e = 8 * i; e < 8 * i + 8; ++e)
-                                        top = fmaxf(top, e > seen ? -INFINITY : fmaf(__uint_as_float(x[e]), m, f.y));
+                                        for (int e = 8 * i; e < 8 * i + 8; ++e)
+                                            top = fmaxf(top, e > seen ? -INFINITY : fmaf(__uint_as_float(x[e]), m, f.y));
+                                    }
                                 }
-                            }
-                            float *slot = xchg + 128 * g + row;
-                            if (h == 1) *slot = top;
-                            named_bar_sync(pair_bar, 64);
-                            if (h == 0) *slot = top = fmaxf(top, *slot);
-                            named_bar_sync(pair_bar, 64);
-                            if (h == 1) top = *slot;
-                            float alpha = 1.f;
-                            if (top > ref + kRefMove) {  // any maximum, where there is no reference yet
-                                alpha = fast_exp2(ref - (top - kRefDrop));
-                                ref = top - kRefDrop;
-                                l *= alpha;
-                            }
-                            if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                                // S of this tile is complete, hence every earlier PV of the group
+                                float *slot = xchg + 128 * g + row;
+                                if (h == 1) *slot = top;
+                                named_bar_sync(pair_bar, 64);
+                                if (h == 0) *slot = top = fmaxf(top, *slot);
+                                named_bar_sync(pair_bar, 64);
+                                if (h == 1) top = *slot;
+                                float alpha = 1.f;
+                                if (top > ref + kRefMove) {  // any maximum, where there is no reference yet
+                                    alpha = fast_exp2(ref - (top - kRefDrop));
+                                    ref = top - kRefDrop;
+                                    l *= alpha;
+                                }
+                                if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                                    // S of this tile is complete, hence every earlier PV of the group
 #pragma unroll 1
-                                for (int c = 0; c < D / 2; c += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32_async(ocol + (uint32_t)c, o);
-                                    tmem_ld32_wait(o);
+                                    for (int c = 0; c < D / 2; c += 32) {
+                                        uint32_t o[32];
+                                        tmem_ld32_async(ocol + (uint32_t)c, o);
+                                        tmem_ld32_wait(o);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tmem_st32(ocol + (uint32_t)c, o);
+                                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                        tmem_st32(ocol + (uint32_t)c, o);
+                                    }
                                 }
+                                pass = 1;  // the next pass is the last
                             }
-                            pass = 1;  // the next pass is the last
+                            l += share;
+                            if constexpr (decltype(far_c)::value) {
+                                // each P in two bfloat16 numbers, over the scores: of 16 tokens the first in eight columns, the second in eight
+                                const float nref = ref == -INFINITY ? 0.f : -ref;
+#pragma unroll 1
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t x[16], y[16];
+                                    tmem_ld16(scol + 16u * c, x);
+                                    const int seen = limit() - token(jj) - 16 * c;
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
+                                        const float4 f = fac[2 * c + e / 8];
+                                        const float e0 = e > seen ? 0.f : fast_exp2(fmaf(__uint_as_float(x[e]), mul * f.x, f.y + nref));
+                                        const float e1 = e + 1 > seen ? 0.f : fast_exp2(fmaf(__uint_as_float(x[e + 1]), mul * f.x, f.y + nref));
+                                        y[e / 2] = pack2<true>(e0, e1);
+                                        y[8 + e / 2] = pack2<true>(e0 - __uint_as_float(y[e / 2] << 16), e1 - __uint_as_float(y[e / 2] & 0xffff0000u));
+                                    }
+                                    tmem_st16(scol + 16u * c, y);
+                                }
+                            } else {
+                                tmem_st32(scol, pk);  // over the first half of the scores it read
+                            }
+                            tmem_wait_st();
                         }
-                        l += share;
-                        tmem_st32(scol, pk);  // over the first half of the scores it read
-                        tmem_wait_st();
+                        fs += dual ? 1 : 2;
+                        if (fs >= C::NF) fs -= C::NF;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(at + C::P_READY + 8 * g);
                     }
-                    fs += dual ? 1 : 2;
-                    if (fs >= C::NF) fs -= C::NF;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(at + C::P_READY + 8 * g);
-                }
+                };
+                if (__any_sync(0xffffffffu, seg_far(sg))) tiles(std::true_type());
+                else tiles(std::false_type());
                 fs0 = (fs0 + n) % C::NF;
                 ptc_finish<D, BF16>(p, w, sched, xchg, at + C::O_DONE, at + C::O_FREE, tlane, g, h, row, n, nx, dual, live, warp_live, rho, ref, l, oph, ok, wait);
                 named_bar_sync(1, 512);  // the segment has been read

@@ -19,6 +19,21 @@ namespace gqaq {
 // places above where 32-bit floats end. 448 * 2^48 is 1.3e17.
 constexpr int kLeastPageExp = -48, kMostPageExp = 48;
 
+// A weight is rounded to fp16 relative to 2^-kHeadroom of the row's largest
+// 2^(score + e) so far. Of a token whose page lies at most kHeadroom exponents
+// under the largest so far it keeps what 16-bit pages' weights keep: fp16's 11
+// bits down to 2^-14 of the row's largest softmax weight, and 2^-25 of that where
+// it is less. A page farther down would lose its tokens' bits to a page that may
+// hold nothing in their channels, so its weights are taken in two bfloat16 numbers
+// (off by 2^-17, with the range of 32-bit floats), against its codes in bfloat16,
+// which are exact too.
+constexpr float kHeadroom = 6.f;
+
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x) {
+    const float2 f = half2_bits_to_float2(x);
+    return pack2<true>(f.x, f.y);
+}
+
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // The least exponent whose largest value, 448 * 2^e, reaches `amax` (its bits;
@@ -51,7 +66,8 @@ __device__ __forceinline__ uint32_t e4m3x4_shift(uint32_t w, float by) {
 // what its values add to the argument of the exponential, and the inverse of
 // that, which turns a weight back into its share of the row's sum.
 __device__ __forceinline__ float4 page_factors(int ke, int ve) { return make_float4(pow2i(ke), (float)ve, pow2i(-ve), 0.f); }
-__device__ __forceinline__ float2 page_factors2(int ke, int ve) { return make_float2(pow2i(ke), (float)ve); }  // the first two
+// The first two; the factor negative in a far tile.
+__device__ __forceinline__ float2 page_factors2(int ke, int ve, bool far) { return make_float2(far ? -pow2i(ke) : pow2i(ke), (float)ve); }
 
 // A loader warp's way along an item's pages: 32 table entries at a time, a lane
 // each, with the entries two batches ahead and their pages' exponents one (an
@@ -64,7 +80,10 @@ struct PageFeed {
     int kv;
     int raw;                  // two batches ahead: the entry, if left > -32
     int row1, k1, v1;         // one ahead
+    bool here1;
     int row, ke, ve;          // the batch in use: first row in the pool, exponents
+    int top;                  // largest exponent of values in the item so far
+    bool far;                 // the batch has a page more than kHeadroom under it
 
     __device__ __forceinline__ void entry() {
         if (left > 0) raw = *next;
@@ -75,10 +94,13 @@ struct PageFeed {
         row = row1;
         ke = min(max(k1, kLeastPageExp), kMostPageExp);
         ve = min(max(v1, kLeastPageExp), kMostPageExp);
+        top = max(top, __reduce_max_sync(0xffffffffu, here1 ? ve : kLeastPageExp));
+        far = top - __reduce_min_sync(0xffffffffu, here1 ? ve : kMostPageExp) > (int)kHeadroom;
         const bool here = left > -32, good = (uint32_t)raw < (uint32_t)p.w.num_pages;
         if (ke != k1 || ve != v1 || (here && !good)) raise_flag(p.status, GQAQ_DEV_BAD_PAGE);
         row1 = p.zero_row;
         k1 = v1 = 0;
+        here1 = here;
         if (here && good) {
             const int unit = raw * p.w.Hkv + kv;
             row1 = unit << p.w.shift;
@@ -97,6 +119,8 @@ struct PageFeed {
         raw = 0;
         row1 = p.zero_row;
         k1 = v1 = 0;
+        here1 = false;
+        top = kLeastPageExp;
         entry();
         step(p);
         step(p);

@@ -534,8 +534,9 @@ GQAQ_API int paged_norm_rope_append_e4m3(const gqaq_paged_dims *dims, const gqaq
                                          uint8_t *v_pages, int8_t *k_exp, int8_t *v_exp, void *stream);
 
 /* gqa_paged_attn over 8-bit pages: arguments, workspace and results as there,
- * but that each probability is rounded to fp16 whatever the dtype, relative to
- * the largest weight times 2^v_exp of its row. An exponent outside [-48, 48] is
+ * but that a probability p of a row whose largest is p_max is rounded to within
+ * max(2^-11 p, 2^-25 p_max) whatever the dtype, however far apart the exponents
+ * of the row's pages lie. An exponent outside [-48, 48] is
  * clamped and raises GQAQ_DEV_BAD_PAGE. */
 GQAQ_API int gqa_paged_attn_e4m3(const gqaq_paged_dims *dims, int max_q_len, const gqaq_half *q, const uint8_t *k_pages,
                                  const uint8_t *v_pages, const int8_t *k_exp, const int8_t *v_exp,
