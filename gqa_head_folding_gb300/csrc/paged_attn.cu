@@ -291,7 +291,7 @@ struct PagedWarp8 {
                     for (int i = 0; i < 2; ++i)
                         x[j][i] = pack2<false>(__uint_as_float(x[j][i] << 16) * by, __uint_as_float(x[j][i] & 0xffff0000u) * by);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) mul[b][i] *= __shfl_sync(0xffffffffu, back, 4 * (2 * c + i));
+                for (int i = 0; i < 2; ++i) mul[b][i] = finite32(mul[b][i] * __shfl_sync(0xffffffffu, back, 4 * (2 * c + i)));
             }
             if constexpr (SHARED_Q) {  // each of the eight warps leaves one step for all
 #pragma unroll

@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) {
                                         const float4 f = fac[4 * c + i];
-                                        const float m = mul * f.x, b = f.y + nref;
+                                        const float m = finite32(mul * f.x), b = f.y + nref;
                                         const uint64_t m2 = pair32(m, m), b2 = pair32(b, b);
                                         uint64_t s8 = 0;
 #pragma unroll
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) {
                                         const float4 f = fac[4 * c + i];
-                                        const float m = mul * f.x;
+                                        const float m = finite32(mul * f.x);
 #pragma unroll
                                         for (int e = 8 * i; e < 8 * i + 8; ++e)
                                             top = fmaxf(top, e > seen ? -INFINITY : fmaf(__uint_as_float(x[e]), m, f.y));
@@ -749,8 +749,9 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
 #pragma unroll
                                     for (int e = 0; e < 16; e += 2) {
                                         const float4 f = fac[2 * c + e / 8];
-                                        const float e0 = e > seen ? 0.f : fast_exp2(fmaf(__uint_as_float(x[e]), mul * f.x, f.y + nref));
-                                        const float e1 = e + 1 > seen ? 0.f : fast_exp2(fmaf(__uint_as_float(x[e + 1]), mul * f.x, f.y + nref));
+                                        const float m = finite32(mul * f.x), b = f.y + nref;
+                                        const float e0 = e > seen ? 0.f : fast_exp2(fmaf(__uint_as_float(x[e]), m, b));
+                                        const float e1 = e + 1 > seen ? 0.f : fast_exp2(fmaf(__uint_as_float(x[e + 1]), m, b));
                                         y[e / 2] = pack2<true>(e0, e1);
                                         y[8 + e / 2] = pack2<true>(e0 - __uint_as_float(y[e / 2] << 16), e1 - __uint_as_float(y[e / 2] & 0xffff0000u));
                                     }

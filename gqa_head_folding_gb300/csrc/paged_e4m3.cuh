@@ -36,6 +36,13 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x) {
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
+// A score's factor past the range of 32 bits stays a number, so that a score of zero stays zero.
+__device__ __forceinline__ float finite32(float x) {
+    float r;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(__int_as_float(0x7f7fffff)));
+    return r;
+}
+
 // The least exponent whose largest value, 448 * 2^e, reaches `amax` (its bits;
 // finite, not negative), within the range.
 __device__ __forceinline__ int page_exp_of(uint32_t amax) {

@@ -5,6 +5,7 @@ import torch
 
 import gqa_head_folding_gb300 as g
 from _paged import DTYPES
+from _paged_e4m3 import quantized_inputs
 from _paged_e4m3_far import channels_by_level, one_large_channel, ref_far
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +68,14 @@ def test_half_of_a_small_page(low, D):
         out = check((q, kp, ke, vp, ve, table, cu, kv), 0.1)
         last = out[[n - 1, 2 * n - 1]].double() * 2.0 ** -low
         assert ((last - 0.5).abs() <= 0.5 * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("size, ke, scale", [(2.0 ** 100, 48, 0.125), (2.0 ** 127, 0, 2.0 ** 20), (-2.0 ** 110, 30, -1.0), (2.0 ** 127, -48, 1.0)])
+@pytest.mark.parametrize("q_lens, kv_lens, G", STEPS)
+def test_keys_of_zero_meet_huge_queries(size, ke, scale, q_lens, kv_lens, G):
+    """A product of zero is zero, however large the factor that it is taken times."""
+    x = list(quantized_inputs(q_lens, kv_lens, 2 * G, 2, 64, 16, torch.bfloat16, 3, DEV))
+    x[0].fill_(size)
+    x[1] = torch.where(x[1] == 127, x[1], torch.zeros_like(x[1]))
+    x[2] = torch.where(x[2] == -128, x[2], torch.full_like(x[2], ke))
+    check(x, scale)
