@@ -274,10 +274,11 @@ __device__ __forceinline__ void pdl_wait_and_release() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-// The two halves, for a kernel that depends on its predecessor's predecessor
-// alone (whose grid has ended when the predecessor releases its dependents): it
-// may run beside the predecessor, and waits for it before it ends, so that what
-// comes next finds both done.
+// The two halves, for two launches of one call that run side by side. The first
+// waits, says in device memory that it has (store_release_gpu) and releases its
+// dependents; the second reads that (load_acquire_gpu) before it touches what the
+// call's predecessors wrote, since its own wait is for the whole first launch, and
+// waits before it ends, so that what comes next finds both done.
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -288,6 +289,15 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned *ptr, unsign
     unsigned old;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(ptr), "r"(v) : "memory");
     return old;
+}
+
+__device__ __forceinline__ void store_release_gpu(unsigned *ptr, unsigned v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(ptr), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned load_acquire_gpu(const unsigned *ptr) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void raise_flag(int *status, int flag) {

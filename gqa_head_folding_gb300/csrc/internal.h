@@ -206,6 +206,9 @@ size_t paged_attn_workspace_bytes(const gqaq_paged_dims *dims, const LaunchCtx &
 // Its kernels. The workspace holds arrival counters (one word per CTA, zero
 // between calls) in its first kPagedCountBytes, then the partials.
 constexpr size_t kPagedCountBytes = GQAQ_PAGED_COUNTER_BYTES;
+// Words of them that two launches side by side meet in: whether the first has waited for what comes before the call, and the
+// second's CTAs that have read that.
+constexpr size_t kPagedBegunWord = kPagedCountBytes / 4 - 2, kPagedReadWord = kPagedCountBytes / 4 - 1;
 int paged_tc_grid(const LaunchCtx &ctx);
 int launch_paged_tc(const PagedAttnArgs &a, const LaunchCtx &ctx);
 int launch_paged_tc_e4m3(const PagedAttnArgs &a, const LaunchCtx &ctx);  // 8-bit pages

@@ -84,7 +84,7 @@ struct PdParams {
     uint64_t timeout_ns;
     int test_stall;
     const int8_t *k_exp, *v_exp;  // 8-bit pages
-    int beside;                   // the launch before is of the same call: this one may run beside it
+    unsigned *begun, *read;       // not null: the launch before is of the same call, and this one may run beside it
 };
 
 template <bool BF16>
@@ -520,8 +520,18 @@ __device__ __forceinline__ void paged_decode(const CUtensorMap &kmap, const CUte
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
-    if (p.beside) pdl_release();
-    else pdl_wait_and_release();
+    if (p.begun != nullptr) {
+        pdl_release();
+        // A loader's thread. It was set before this launch was released; no launch waits for it: where it is not seen, the
+        // whole of the launch before is waited for. (Always waiting so: mixed batches of 32 with two chunks of 500 tokens 83 us
+        // for 81, of 4 with one of 40 tokens 36 for 27; reading the call's inputs without it 80 and 27.)
+        if (tid == 256 && load_acquire_gpu(p.begun) == 0u) pdl_wait();
+        __syncthreads();
+        // the last CTA to have read it takes it back, beside the schedule
+        if (tid == 256 && atomic_add_acq_rel_gpu(p.read, 1u) + 1u == gridDim.x) *p.begun = *p.read = 0u;
+    } else {
+        pdl_wait_and_release();
+    }
     paged_schedule(p.w, sched, scratch, kMinUnits, 0);
     if (warp < 8) paged_zero_rows(p.w, reinterpret_cast<uint4 *>(p.out), p.Hq * D / 8, p.status, 256);
     if (sched->t_begin >= sched->t_end) return;
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(PdCfg<D, KV8, NB>::THREADS, PdCfg<D, KV8, NB>:
     paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ PdParams p) {
     paged_decode<D, BF16, KV8, NB>(kmap, vmap, p);
-    if (p.beside && threadIdx.x == 0) pdl_wait();
+    if (p.begun != nullptr && threadIdx.x == 0) pdl_wait();
 }
 
 template <int D, bool BF16, bool KV8, int NB>
@@ -800,7 +810,8 @@ template <int D, bool BF16, bool KV8, int NB>
 int launch_decode(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     using C = PdCfg<D, KV8, NB>;
     const gqaq_paged_dims &d = *a.dims;
-    const int grid = decode_grid<D, BF16, KV8, NB>(ctx);
+    const bool beside = a.share == 1;
+    const int grid = std::min(decode_grid<D, BF16, KV8, NB>(ctx), (int)(kPagedCountBytes / 8 - (beside ? 2 : 0)));  // a counter each
     if (grid < 1) return GQAQ_ERR_CUDA;
     const uint64_t rows = (uint64_t)d.num_pages * d.num_kv_heads * d.page_size;
     CUtensorMap kmap, vmap;
@@ -817,9 +828,11 @@ int launch_decode(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     p.q = static_cast<const uint16_t *>(a.q);
     p.out = static_cast<uint16_t *>(a.out);
     // beside another launch's: the second half of the counters, and what lies behind its partials
-    p.beside = a.share == 1;
-    p.count = reinterpret_cast<unsigned *>(a.workspace) + (p.beside ? kPagedCountBytes / 8 : 0);
-    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + (p.beside ? paged_tc_workspace_bytes(&d, ctx) : kPagedCountBytes));
+    unsigned *counters = reinterpret_cast<unsigned *>(a.workspace);
+    p.begun = beside ? counters + kPagedBegunWord : nullptr;
+    p.read = beside ? counters + kPagedReadWord : nullptr;
+    p.count = counters + (beside ? kPagedCountBytes / 8 : 0);
+    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + (beside ? paged_tc_workspace_bytes(&d, ctx) : kPagedCountBytes));
     p.status = ctx.status;
     p.gshift = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
     p.Hq = d.num_q_heads;

@@ -88,6 +88,7 @@ static_assert(kRefDrop >= kHeadroom, "the largest weight of a row");
 struct P8Params : PtcParams {
     const int8_t *k_exp, *v_exp;
     int one_tile;  // no item has more than 128 rows
+    unsigned *begun;  // not null: another launch of this call runs beside this one
 };
 
 template <int D>
@@ -249,7 +250,11 @@ __global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem8 + C::AT_SLOT)), "n"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    pdl_wait_and_release();
+    pdl_wait();
+    if (threadIdx.x == 0) {  // the launch beside this one may begin when every CTA has waited, and reads what they waited for
+        if (p.begun != nullptr && blockIdx.x == 0) store_release_gpu(p.begun, 1u);
+        pdl_release();
+    }
     tc_fence_before();
     paged_schedule(p.w, sched, scratch, kMinUnits, D / 64);
     tc_fence_after();
@@ -803,6 +808,7 @@ int launch_t(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     fill_ptc(a, ctx, p);
     p.k_exp = a.k_exp;
     p.v_exp = a.v_exp;
+    p.begun = a.share == 2 ? reinterpret_cast<unsigned *>(a.workspace) + kPagedBegunWord : nullptr;
     p.one_tile = (int64_t)a.max_q_len * p.G <= 128;
     CUtensorMap qmap, kmap, vmap;
     if (!encode_tensor_map_heads(&qmap, a.q, d.max_tokens, d.num_q_heads, D, p.G, 128 / p.G)) return GQAQ_ERR_CUDA;
