@@ -73,3 +73,14 @@ def channels_by_level(q_lens, kv_lens, G, D, S, dtype, levels, seed, device):
     x[3] = torch.where(keep, vp, torch.zeros_like(vp))
     x[4] = torch.where(ve == -128, ve, torch.tensor(levels, device=device)[level].to(torch.int8))
     return x
+
+
+def wide_rows_of_q(q_lens, kv_lens, G, D, S, seed, device):
+    """bfloat16 rows whose first channels are up to 2^40 times the others, over keys that are zero in those: the small channels
+    decide the scores."""
+    x = list(quantized_inputs(q_lens, kv_lens, 2 * G, 2, D, S, torch.bfloat16, seed, device))
+    q, kp = x[0].float(), x[1]
+    q[..., :8] *= pow2(torch.arange(8, device=device) * 5 + 5).float()
+    kp[..., :8] = torch.where(kp[..., :8] == 127, kp[..., :8], torch.zeros_like(kp[..., :8]))
+    x[0] = q.bfloat16()
+    return x
