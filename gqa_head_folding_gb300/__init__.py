@@ -901,7 +901,9 @@ def paged_norm_rope_append_e4m3(q, k, v, positions, slots, k_pages, v_pages, k_e
                                 eps: float = 1e-6, cos_sin=None, interleaved: bool = False, q_out=None):
     """paged_norm_rope_append to 8-bit pages (codes uint8, exponents [num_pages,Hkv] int8; see new_pages_e4m3): a
     page's exponent covers its largest magnitude. Rows that join a page may raise it, and the codes there are then
-    rounded again; rows from a page's first one on start it afresh. The tokens of a page lie one behind the other."""
+    rounded again; rows from a page's first one on start it afresh, and until then it never falls, also when the rows
+    that raised it have been released. Infinities become the page's largest number; NaN stays. The tokens of a page lie
+    one behind the other."""
     return _paged_append("paged_norm_rope_append_e4m3", q, k, v, positions, slots, (k_pages, v_pages), torch.uint8, (k_exp, v_exp),
                          q_weight, k_weight, eps, cos_sin, interleaved, q_out)
 

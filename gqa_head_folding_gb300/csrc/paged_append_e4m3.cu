@@ -2,7 +2,8 @@
 // tokens to 8-bit pages (paged_e4m3.cuh).
 //
 // A run is the step's tokens of one page: consecutive rows whose slots ascend
-// by one (one of them without an angle is skipped, and the run goes on). For each run and KV head, of keys and of values alike:
+// by one (one of them without an angle is skipped, and the run goes on). For each
+// run and KV head, of keys and of values alike:
 //   a    = the largest finite |y| of the run's rows (fp32, after norm and rotation)
 //   e    = the least exponent with a <= 448 * 2^e; of a page that holds rows (the
 //          run does not begin at its row 0) at least the exponent it has
@@ -26,7 +27,13 @@
 // of slots, rows, maxima, exponents and codes, each of which waits for the one
 // before, beside 17 instructions per channel (55% of the issue slots; a third
 // are conversions and moves between register pairs). A small step is that chain
-// once (32 single tokens 5.2 us, four chunks among 19 single tokens 9.0).
+// once (32 single tokens 5.2 us; four chunks among 19 single tokens over pages of
+// 64, which are two windows of 128 channels and computed twice, 9.0), where no
+// page's exponent grows. A window's grown pages are rounded again by its one CTA,
+// 16 bytes a thread after the other: where all pages of 32 single tokens grow, 8
+// and 12 us (64 and 128 channels, pages of 16), 17 and 29 (of 64), 28 and 50 (of
+// 128); of 256 single tokens 14 and 15, 38 and 42, 66 and 76; of 16 times 5 drafted
+// tokens 9 and 8, 13 and 12, 18 and 17.
 #include "paged_e4m3.cuh"
 #include "paged_rows.cuh"
 
@@ -35,9 +42,10 @@ namespace {
 
 // Threads of a CTA, those of an SM, and the query rows that a lane has in flight. A step whose CTAs all run at once asks for
 // all it needs at the start. A longer one gains more from half as long windows and six CTAs per SM, which are at different
-// stages, though each has fewer rows in flight (32 query and 8 KV heads of 128 channels: 1024 tokens 7.1 us against 9.0, 1500
-// tokens 10.7 against 9.3, 8000 tokens 48.7 against 43.3). Pages longer than such a window stay with the long one: a run's
-// rows beyond the first pass are read twice.
+// stages, though each has fewer rows in flight (32 query and 8 KV heads of 128 channels, pages of 16: 1024 tokens 7.1 us
+// against 9.0, 1500 tokens 10.7 against 9.3, 8000 tokens 48.7 against 43.3). Pages longer than such a window stay with the long
+// one: a run's rows beyond the first pass are read and computed twice (8192 tokens, long against short windows: 128 channels,
+// pages of 32, 64 and 128 50, 54 and 59 us against 47, 52 and 61; 64 channels, of 64 and 128 26 and 29 against 27 and 32).
 struct FewTokens {
     static constexpr int THREADS = 256, RESIDENT = 512, AHEAD = 4;
 };

@@ -10,12 +10,14 @@
 // with an online softmax in the log2 domain on the S^T fragments: the row
 // maxima are gathered across lanes, and the sums and outputs rescaled, only
 // when a tile holds a score 2^8 above the reference (P <= 2^8 keeps fp16
-// exact enough). Sums and outputs are fp32; each P is rounded once.
+// exact enough). Sums and outputs are fp32; each P is rounded once (over 8-bit
+// pages: see PagedWarp8).
 //
 // Kernel shape (persistent CTAs, one launch): the tiles of 128 tokens of all
 // (request, KV head) items are split evenly (paged_sched.cuh); warp 8 gathers
 // a tile from its pages with TMA, one box per page and operand, into a ring of
-// three stages; warps 0-7 own 16 tokens of each tile. At the end of an item's
+// stages (three over 16-bit pages, three to ten over 8-bit ones); warps 0-7 own 16
+// tokens of each tile. At the end of an item's
 // segment the eight warps' states merge in shared memory; an item cut by a
 // range boundary leaves an fp32 partial and the CTA that arrives last merges
 // them.
@@ -27,8 +29,8 @@
 //
 // Over 8-bit pages the codes are widened to fp16 between shared memory and the
 // product, by the lane that needs them, once for all blocks of eight rows. Half
-// the bytes: the batch of 8 at up to 64K takes 132 to 135 us (5.7 TB/s, 83% of the
-// copy rate, 48% of the issue slots), with two CTAs per SM (one with five stages
+// the bytes: the batch of 8 at up to 64K takes 132 us (5.7 TB/s, 85% of the
+// copy rate, 49% of the issue slots), with two CTAs per SM (one with five stages
 // 139), one request at 4K 10.1. Two 16s of tokens per warp and tile, whose products
 // are independent, were no faster at 64 channels (one request 10.7 us, 32 of 1K to 4K 29.7
 // for 28.9) and spill at 128.
@@ -198,7 +200,7 @@ struct PagedWarp {
             mma16<BF16>(o[i], a, pb0, pb1);
         }
     }
-    // (m, l, acc) of rows first .. first + 3 to this warp's slot of the merge buffer.
+    // (m, l, acc) of rows first .. first + MROWS - 1 to this warp's slot of the merge buffer.
     __device__ __forceinline__ void store(float *slot, int, int first) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -232,8 +234,8 @@ struct PagedWarp {
 // context begins with such a large page. A tile's whole work in two copies costs
 // nothing where there is none; one copy with a branch before V took 147. Queries
 // are fp16 there too: a bfloat16 row is taken times a power of two that brings its
-// largest channel under 2^15 (a channel 2^-38 of that and less loses bits, 2^-40
-// of the score's terms).
+// largest channel into [2^14, 2^15): channels down to 2^-31 of it keep all their
+// bits, smaller ones are off by at most 2^-39 of it.
 // Lane r * 4 + c reads bytes D/4 c .. of K rows r and r + 8, and bytes D/8 r ..
 // of V rows 2c, 2c + 1, 2c + 8 and 2c + 9: channel (D/4) c + 4 j + e of q meets
 // its like in step j, and channel (D/8) r + 2 i + h of O lies in o[i][2 h], o[i][2 h + 1].
@@ -670,7 +672,7 @@ __device__ __forceinline__ void paged_decode(const CUtensorMap &kmap, const CUte
             if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
         }
 
-        // ---- merge the eight warps' states, four rows at a time ----
+        // ---- merge the eight warps' states, MROWS rows at a time ----
         const int64_t out0 = ((int64_t)w.s.q0 * p.Hq + (w.kv << p.gshift)) * D;
         float *part = p.part + ((int64_t)blockIdx.x * 2 + w.slot()) * C::PART;
 #pragma unroll
@@ -848,10 +850,15 @@ int launch_decode(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     return e == cudaSuccess ? GQAQ_OK : GQAQ_ERR_CUDA;
 }
 
-// Blocks of eight rows that the decode kernel takes over 8-bit pages, both sides measured against the tensor-memory kernel (32 query and 8
-// KV heads, bf16, 32 requests of 500 to 4K): 64 channels, 1 to 4 blocks 28, 39, 45 and 57 us against 59; 128 channels, 1 to
-// 3 blocks 47, 53 and 64 against 72. More do not fit the registers. One request at 4K, whose parts one CTA merges: 64
-// channels, 3 and 4 blocks 16 and 23 us against 19; 128 channels, 3 blocks 26 against 25.
+// Blocks of eight rows that the decode kernel takes over 8-bit pages, both sides measured against the tensor-memory
+// kernel (four query heads per KV head, bf16). 32 requests of 500 to 4K, 8 KV heads: 64 channels, 1 to 4 blocks 28, 39, 45
+// and 57 us against 59; 128 channels, 1 to 3 blocks 47, 53 and 64 against 72. More do not fit the registers. Few requests
+// at 4K, whose parts one CTA merges: 64 channels, 3 blocks 16 to 19 against 19 to 26; 4 blocks, one request 21 to 24 against 19
+// to 20, two requests or eight on one KV head 23 and 24 against 23, four on eight 23 against 26; 128 channels, 2 blocks 19 to
+// 22 against 25 to 32, 3 blocks of one request 25 to 26 on either side, of more 26 to 27 against 28 to 33. So only
+// the fourth block of a single request goes to the other kernel. One number serves the whole batch, from max_q_len, so
+// requests of fewer rows compute with the blocks of the longest (of 500 to 4K, 64 and 128 channels: 32 single tokens 27 and
+// 41 us, 31 and one of five tokens 47 and 63, 32 of five 47 and 64).
 constexpr int kMostBlocks64 = 4, kMostBlocks128 = 3;
 int most_blocks(const gqaq_paged_dims &d) { return d.head_dim == 128 ? kMostBlocks128 : d.batch == 1 ? kMostBlocks64 - 1 : kMostBlocks64; }
 
@@ -874,7 +881,13 @@ int launch_rows16(const PagedAttnArgs &a, const LaunchCtx &ctx) {  // 16-bit pag
     return a.dims->head_dim == 128 ? launch_blocks<128, false, 1>(a, ctx) : launch_blocks<64, false, 1>(a, ctx);
 }
 int launch_rows8(const PagedAttnArgs &a, int blocks, const LaunchCtx &ctx) {  // 8-bit pages
-    if (a.dims->head_dim == 128) return blocks == 1 ? launch_blocks<128, true, 1>(a, ctx) : blocks == 2 ? launch_blocks<128, true, 2>(a, ctx) : launch_blocks<128, true, 3>(a, ctx);
+    if (a.dims->head_dim == 128) {
+        switch (blocks) {
+            case 1: return launch_blocks<128, true, 1>(a, ctx);
+            case 2: return launch_blocks<128, true, 2>(a, ctx);
+            default: return launch_blocks<128, true, 3>(a, ctx);
+        }
+    }
     switch (blocks) {
         case 1: return launch_blocks<64, true, 1>(a, ctx);
         case 2: return launch_blocks<64, true, 2>(a, ctx);
@@ -900,7 +913,9 @@ int launch_paged_attn(const PagedAttnArgs &a, const LaunchCtx &ctx) {
     if (a.k_exp == nullptr) return rows > kRows ? launch_paged_tc(a, ctx) : launch_rows16(a, ctx);
     if (rows <= most_blocks(*a.dims) * kRows) return launch_rows8(a, (int)(rows + kRows - 1) / kRows, ctx);
     if (a.dims->batch == 1) return launch_paged_tc_e4m3(a, ctx);
-    // Over 8-bit pages a batch may hold both: each request goes to its kernel by its own rows, in two launches side by side.
+    // Over 8-bit pages a batch whose longest request goes there may hold short ones too: those of up to eight rows go to the
+    // decode kernel, by their own rows, in a launch beside it (a mixed batch 107 -> 81 us; the two alone 60 and 23). One of nine
+    // rows and more shares the tensor-memory kernel, where it costs a row tile.
     PagedAttnArgs part = a;
     part.share = 2;
     const int rc = launch_paged_tc_e4m3(part, ctx);

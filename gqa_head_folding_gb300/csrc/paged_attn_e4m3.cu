@@ -15,10 +15,10 @@
 // below takes 944 us for 441 where every segment has such pages. Each role's loop in
 // two copies costs 3 us there; a flag per tile, read in one loop, took 502 to 532.
 // The products of scores are fp16 whatever the dtype: a bfloat16 row of q is taken
-// times a power of two that brings its largest channel under 2^15 (a channel 2^-38
-// of that and less loses bits, 2^-40 of the score's terms), since both operands of
-// a product have one type and a code costs a conversion more to bfloat16. The
-// reference moves as in paged_attn_tc.cu.
+// times a power of two that brings its largest channel into [2^14, 2^15) (channels
+// down to 2^-31 of it keep all their bits, smaller ones are off by at most 2^-39 of
+// it), since both operands of a product have one type and a code costs a
+// conversion more to bfloat16. The reference moves as in paged_attn_tc.cu.
 //
 // Kernel shape: that of paged_attn_tc.cu (items of 256 rows, two softmax groups
 // with S and O in tensor memory, the notifier, the same end of an item), with
@@ -33,7 +33,7 @@
 //    the softmax warps have no room to give (they hold 96, the others 48).
 //
 // What bounds it. A 1024-token chunk of a 32K context (32 heads of 128 channels):
-// 441 us, 1,230 TFLOP/s, 63% of a large library product's rate; the tensor pipe is busy 53% of
+// 441 us, 1,230 TFLOP/s, 63% of a large library product's rate; the tensor pipe is busy 52% of
 // the cycles and the exponentials 26%, and the rest is the chain S, softmax, PV of
 // the two row tiles. Sixteen requests of up to 9K tokens with seven drafted tokens
 // (28 live rows of 128; 8 KV heads of 128 channels): 69 us for 25 us of bytes.

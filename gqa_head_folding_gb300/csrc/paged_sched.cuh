@@ -20,7 +20,7 @@ namespace gqaq {
 
 constexpr int kPagedTileLog = 7, kPagedTile = 1 << kPagedTileLog;
 
-constexpr int kFewRows = 8;  // of a KV head: what the decode kernels take
+constexpr int kFewRows = 8;  // of a KV head: a block of the decode kernel, and what shares a batch with longer requests without joining them
 
 struct PagedWorkParams {
     const int *table, *cu_q, *kv_len;

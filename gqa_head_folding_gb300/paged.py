@@ -35,7 +35,9 @@ class PagedCache:
     given (max_tokens, or fewer); rows behind the step's tokens are padding.
 
     ``dtype`` is the type of q, k and v, and of the pages unless ``kv_dtype`` says torch.float8_e4m3fn: then
-    k_pages and v_pages hold E4M3 codes, k_exp and v_exp the exponents of each layer's pages."""
+    k_pages and v_pages hold E4M3 codes, k_exp and v_exp the exponents of each layer's pages. A released tail of large
+    rows (a rejected draft) leaves the exponent of the page it began in where it put it: rows that join the page later are
+    rounded to it, until the page is begun again. Infinite keys and values become their page's largest number."""
 
     def __init__(self, num_layers: int, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, pool_pages: int,
                  max_len: int, max_tokens: int, device, page_size: int = PAGE_SIZE, dtype=torch.float16, kv_dtype=None):

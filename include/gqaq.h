@@ -523,7 +523,10 @@ GQAQ_API int gqa_paged_attn(const gqaq_paged_dims *dims, int max_q_len, const gq
  *     beyond 448 * 2^exp (infinities) saturate, NaN stays
  * Where a page's exponent grows by n, the codes of its other rows become the
  * codes nearest to value / 2^n: only those that fall under E4M3's smallest
- * normal number lose anything. Two runs of one call must not lie in the same
+ * normal number lose anything. It never falls: a page keeps the exponent that a
+ * large row gave it after that row has been released (a rejected draft), and what
+ * is rounded to it, until a run begins the page again. An infinity becomes the
+ * finite number 448 * 2^exp here, and raises no flag. Two runs of one call must not lie in the same
  * page. k_pages and v_pages (and k_exp and v_exp) must not overlap. q_out, and
  * all else, as paged_norm_rope_append. */
 GQAQ_API int paged_norm_rope_append_e4m3(const gqaq_paged_dims *dims, const gqaq_half *q, int64_t q_stride,
@@ -536,7 +539,10 @@ GQAQ_API int paged_norm_rope_append_e4m3(const gqaq_paged_dims *dims, const gqaq
 /* gqa_paged_attn over 8-bit pages: arguments, workspace and results as there,
  * but that a probability p of a row whose largest is p_max is rounded to within
  * max(2^-11 p, 2^-25 p_max) whatever the dtype, however far apart the exponents
- * of the row's pages lie. An exponent outside [-48, 48] is
+ * of the row's pages lie, and that a channel of a bfloat16 row of q is off by up to
+ * 2^-39 of the row's largest. The last bits of a request's output may depend on its
+ * batch: max_q_len and the other requests' lengths say which kernel computes it and
+ * where its context is cut. An exponent outside [-48, 48] is
  * clamped and raises GQAQ_DEV_BAD_PAGE. */
 GQAQ_API int gqa_paged_attn_e4m3(const gqaq_paged_dims *dims, int max_q_len, const gqaq_half *q, const uint8_t *k_pages,
                                  const uint8_t *v_pages, const int8_t *k_exp, const int8_t *v_exp,
